@@ -235,4 +235,39 @@ cudaError_t launch_lin_bwd_kv(const void* k, const void* v, const float* dhm,
                               float* dk, float* dv, const Geom& g,
                               cudaStream_t s);
 
+// Rotary positions (rotary.cu): raw[i] <-> rot[i] for `tensors` tensors;
+// raw_strides in elements.
+cudaError_t launch_rotary(const Geom& g, const sla_rotary& r, const i64* raw_strides, void* const* raw,
+                          void* const* rot, int tensors, bool rot_f32, const int32_t* positions,
+                          bool pos_batched, const int32_t* perm, bool inverse, cudaStream_t s);
+
+// Linear attention with a decay for each head (decay_kernels.cu says what the
+// roles and segments are).
+struct DecayPlan {
+  int N, H;
+  int seg_len, segs;  // tokens per segment (a multiple of the chunk), segments
+};
+struct DecayRole {
+  float w_in, w_st, w_sum;  // factors of the pairs, of the state, of what the state takes up
+  int e;                    // 1: the state already holds its own token
+  bool reverse;             // last token to first
+  bool transposed;          // the stored state is the transpose of the one used
+};
+// `zero`, if given, is a status word that the launch clears.
+int decay_simt_chunk();
+cudaError_t launch_decay_sums_simt(const void* b, const void* c, const float* log_decay,
+                                   const int32_t* lens, float* sums, const DecayPlan& P, int e,
+                                   bool reverse, float w_sum, const Geom& g, int32_t* zero,
+                                   cudaStream_t s);
+cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, const float* log_decay,
+                                  const int32_t* lens, const float* starts, i64 start_stride, void* out,
+                                  float* final_state, const DecayPlan& P, const DecayRole& R,
+                                  const Geom& g, int32_t* zero, cudaStream_t s);
+cudaError_t launch_decay_scan(float* sums, const float* first, float* final_state,
+                              const float* log_decay, const int32_t* lens, const DecayPlan& P,
+                              bool reverse, const Geom& g, cudaStream_t s);
+cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                              const int32_t* lens, const float* state_in, float* state_out, void* out,
+                              const Geom& g, int32_t* zero, cudaStream_t s);
+
 }  // namespace sla

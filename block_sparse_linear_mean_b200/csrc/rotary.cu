@@ -1,0 +1,308 @@
+// Rotary positions: q and k turned by their tokens' positions, and their
+// gradients back.
+//
+// Pair (a, b) of a token at position x turns by the angle x w:
+//   a' = m (a cos - b sin),  b' = m (b cos + a sin);   the transpose (the
+// gradient) has -sin.  The pass reads the projection's layout (any strides),
+// takes tokens into another order on the way and writes the dense [B,H,N,d]
+// that mask and attention read, or goes the other way.
+//
+// Angles: x w is formed in 64 bits and reduced to a fraction of a turn there,
+// so a position of a million still has its phase to 2^-25 of a turn (in 32
+// bits the product alone would be off by 0.03 rad); sine and cosine of the
+// fraction are fp32.  They are shared by all heads, so a thread keeps the
+// cosines of its few pairs of one token in registers and walks over the heads
+// of both tensors: one 64-bit angle per (token, pair), not per value.
+//
+// Bound by HBM: every value is read once and written once.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace sla {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 64;
+constexpr int kRows = 4;  // rows in flight per thread
+
+// The side that is read and the side that is written, in elements.
+struct Side {
+  i64 b, h, n;
+};
+
+struct RotaryArgs {
+  const void* src[2];
+  void* dst[2];
+  Side in, out;
+  const int32_t* positions;  // [axes, N] or [B, axes, N]
+  const int32_t* perm;
+  i64 tokens;                // B * N
+  int N, H, d;
+  int tensors;               // 1 or 2
+  int rows_per_group;        // rows = (tensor, head) pairs per blockIdx.y
+  int pairs, axes;
+  int split1, split2;        // first pair of axes 1 and 2
+  int grid_r, grid_c;
+  int origin[3];
+  int pos_batched;
+  int gather;                // perm on the read side (forward) or the written one
+  float sign, amplitude;
+  double turns[kMaxPairs];   // freq / 2 pi
+};
+
+// V consecutive elements of a row as fp32, in accesses of at most 16 bytes.
+template <int V>
+__device__ __forceinline__ void load_n(const float* p, float* x) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+    }
+  } else if constexpr (V == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    x[0] = f.x; x[1] = f.y;
+  } else {
+    x[0] = *p;
+  }
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float* x) {
+  const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  x[0] = f.x; x[1] = f.y;
+}
+template <int V>
+__device__ __forceinline__ void load_n(const __nv_bfloat16* p, float* x) {
+  if constexpr (V == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    unpack2(u.x, x); unpack2(u.y, x + 2); unpack2(u.z, x + 4); unpack2(u.w, x + 6);
+  } else if constexpr (V == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    unpack2(u.x, x); unpack2(u.y, x + 2);
+  } else if constexpr (V == 2) {
+    unpack2(*reinterpret_cast<const uint32_t*>(p), x);
+  } else {
+    x[0] = __bfloat162float(*p);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_n(float* p, const float* x) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+    *p = x[0];
+  }
+}
+__device__ __forceinline__ uint32_t pack2(const float* x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int V>
+__device__ __forceinline__ void store_n(__nv_bfloat16* p, const float* x) {
+  if constexpr (V == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x), pack2(x + 2), pack2(x + 4), pack2(x + 6));
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x), pack2(x + 2));
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack2(x);
+  } else {
+    *p = __float2bfloat16_rn(x[0]);
+  }
+}
+
+// A unit is V pairs of one token's row (2 V channels); the d / (2 V) units of
+// a row take one thread each.  The first pairs / V of them turn, the rest are
+// copied.  Half layout: channels [a, a + V) and [a + pairs, + V); interleaved:
+// 2 V neighbours.
+template <typename TIn, typename TOut, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs A) {
+  __shared__ double turns[kMaxPairs];
+  if (threadIdx.x < kMaxPairs) turns[threadIdx.x] = A.turns[threadIdx.x];
+  __syncthreads();
+  const int units = A.d / (2 * V);
+  const int per_cta = kThreads / units;
+  const int u = threadIdx.x % units;
+  const i64 tok = i64(blockIdx.x) * per_cta + threadIdx.x / units;
+  if (tok >= A.tokens) return;
+  const i64 b = tok / A.N;
+  const int n = static_cast<int>(tok - b * A.N);
+  int t = n;  // raw token
+  if (A.perm) {
+    t = A.perm[n];
+    if (t < 0 || t >= A.N) return;
+  }
+  const bool turn = u * V < A.pairs;
+  float cs[V], sn[V];
+  if (turn) {
+    i64 pos[3];
+    if (A.positions) {
+      const int32_t* ps = A.positions + (A.pos_batched ? b * A.axes : 0) * A.N + t;
+      pos[0] = ps[0];
+      pos[1] = A.axes > 1 ? ps[A.N] : 0;
+      pos[2] = A.axes > 2 ? ps[i64(A.N) * 2] : 0;
+    } else if (A.axes == 1) {
+      pos[0] = i64(t) + A.origin[0];
+      pos[1] = pos[2] = 0;
+    } else {
+      const int c = t % A.grid_c, fr = t / A.grid_c;
+      if (A.axes == 2) {
+        pos[0] = i64(fr) + A.origin[0];
+        pos[1] = i64(c) + A.origin[1];
+        pos[2] = 0;
+      } else {
+        pos[0] = i64(fr / A.grid_r) + A.origin[0];
+        pos[1] = i64(fr % A.grid_r) + A.origin[1];
+        pos[2] = i64(c) + A.origin[2];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = u * V + i;
+      const i64 x = c < A.split1 ? pos[0] : c < A.split2 ? pos[1] : pos[2];
+      const double ang = static_cast<double>(x) * turns[c];
+      float s, co;
+      sincospif(2.f * static_cast<float>(ang - rint(ang)), &s, &co);
+      cs[i] = co * A.amplitude;
+      sn[i] = s * A.amplitude * A.sign;
+    }
+  }
+  // first channels of the unit's two pieces of V
+  int c0, c1;
+  if (INTER) {
+    c0 = 2 * V * u;
+    c1 = c0 + V;
+  } else if (turn) {
+    c0 = u * V;
+    c1 = c0 + A.pairs;
+  } else {
+    c0 = 2 * A.pairs + 2 * (u * V - A.pairs);
+    c1 = c0 + V;
+  }
+  const int n_in = A.gather ? t : n, n_out = A.gather ? n : t;
+  const i64 in0 = b * A.in.b + n_in * A.in.n, out0 = b * A.out.b + n_out * A.out.n;
+  const int row0 = blockIdx.y * A.rows_per_group;
+  const int row1 = min(row0 + A.rows_per_group, A.tensors * A.H);
+  for (int r0 = row0; r0 < row1; r0 += kRows) {
+    float x[kRows][2 * V];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int r = r0 + k;
+      if (r < row1) {
+        const int second = r >= A.H, h = second ? r - A.H : r;
+        const TIn* src = static_cast<const TIn*>(second ? A.src[1] : A.src[0]) + in0 + h * A.in.h;
+        if (INTER) {
+          load_n<2 * V>(src + c0, x[k]);
+        } else {
+          load_n<V>(src + c0, x[k]);
+          load_n<V>(src + c1, x[k] + V);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int r = r0 + k;
+      if (r < row1) {
+        if (turn) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& a = INTER ? x[k][2 * i] : x[k][i];
+            float& c = INTER ? x[k][2 * i + 1] : x[k][V + i];
+            const float ya = a * cs[i] - c * sn[i], yc = c * cs[i] + a * sn[i];
+            a = ya;
+            c = yc;
+          }
+        }
+        const int second = r >= A.H, h = second ? r - A.H : r;
+        TOut* dst = static_cast<TOut*>(second ? A.dst[1] : A.dst[0]) + out0 + h * A.out.h;
+        if (INTER) {
+          store_n<2 * V>(dst + c0, x[k]);
+        } else {
+          store_n<V>(dst + c0, x[k]);
+          store_n<V>(dst + c1, x[k] + V);
+        }
+      }
+    }
+  }
+}
+
+template <typename TIn, typename TOut, int V, bool INTER>
+cudaError_t launch(RotaryArgs& a, cudaStream_t s) {
+  const int per_cta = kThreads / (a.d / (2 * V));
+  const i64 gx = (a.tokens + per_cta - 1) / per_cta;
+  const int rows = a.tensors * a.H;
+  // few tokens: the rows are spread over more CTAs (their angles are formed
+  // again there), down to two rows each
+  const i64 want = std::max<i64>(1, 148 * 4 / gx);
+  const int groups = static_cast<int>(std::min<i64>(want, std::max(1, rows / 2)));
+  a.rows_per_group = (rows + groups - 1) / groups;
+  const dim3 grid(static_cast<unsigned>(gx), (rows + a.rows_per_group - 1) / a.rows_per_group);
+  rotary_kernel<TIn, TOut, V, INTER><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TIn, typename TOut>
+cudaError_t dispatch(RotaryArgs& a, bool inter, cudaStream_t s) {
+  // the widest pieces that the split at `pairs` allows: 16 bytes of the
+  // narrower type per access
+  constexpr bool wide = sizeof(TIn) == 2 || sizeof(TOut) == 2;
+  const int p = a.pairs;
+  if (inter) {
+    if constexpr (wide)
+      if (p % 4 == 0) return launch<TIn, TOut, 4, true>(a, s);
+    if (p % 2 == 0) return launch<TIn, TOut, 2, true>(a, s);
+    return launch<TIn, TOut, 1, true>(a, s);
+  }
+  if constexpr (wide)
+    if (p % 8 == 0) return launch<TIn, TOut, 8, false>(a, s);
+  if (p % 4 == 0) return launch<TIn, TOut, 4, false>(a, s);
+  if (p % 2 == 0) return launch<TIn, TOut, 2, false>(a, s);
+  return launch<TIn, TOut, 1, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const Geom& g, const sla_rotary& r, const i64* raw_strides, void* const* raw,
+                          void* const* rot, int tensors, bool rot_f32, const int32_t* positions,
+                          bool pos_batched, const int32_t* perm, bool inverse, cudaStream_t s) {
+  RotaryArgs a{};
+  const Side dense{i64(g.H) * g.N * g.d, i64(g.N) * g.d, g.d};
+  const Side rs{raw_strides[0], raw_strides[1], raw_strides[2]};
+  for (int i = 0; i < tensors; ++i) {
+    a.src[i] = inverse ? rot[i] : raw[i];
+    a.dst[i] = inverse ? raw[i] : rot[i];
+  }
+  a.in = inverse ? dense : rs;
+  a.out = inverse ? rs : dense;
+  a.positions = positions;
+  a.perm = perm;
+  a.tokens = i64(g.B) * g.N;
+  a.N = g.N;
+  a.H = g.H;
+  a.d = g.d;
+  a.tensors = tensors;
+  a.pairs = r.rot_dim / 2;
+  a.axes = r.axes;
+  a.split1 = r.axis_pairs[0];
+  a.split2 = r.axis_pairs[0] + r.axis_pairs[1];
+  a.grid_r = std::max(1, r.grid[1]);
+  a.grid_c = std::max(1, r.grid[2]);
+  for (int i = 0; i < 3; ++i) a.origin[i] = r.origin[i];
+  a.pos_batched = pos_batched;
+  a.gather = !inverse;
+  a.sign = inverse ? -1.f : 1.f;
+  a.amplitude = r.amplitude;
+  constexpr double kTurn = 0.15915494309189533577;  // 1 / 2 pi
+  for (int i = 0; i < a.pairs; ++i) a.turns[i] = r.freq[i] * kTurn;
+  const bool inter = r.layout == SLA_ROTARY_INTERLEAVED;
+  using bf = __nv_bfloat16;
+  if (g.dtype == SLA_F32) return dispatch<float, float>(a, inter, s);
+  if (!rot_f32) return dispatch<bf, bf>(a, inter, s);
+  return inverse ? dispatch<float, bf>(a, inter, s) : dispatch<bf, float>(a, inter, s);
+}
+
+}  // namespace sla

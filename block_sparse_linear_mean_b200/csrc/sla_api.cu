@@ -86,6 +86,7 @@ bool has_linear_branch(const Geom& g) { return g.linear; }
 struct MaskWs { size_t qbar, kbar, qlo, klo, logits, total; };
 struct FwdWs { size_t o_s, hsum, zsum, lintc, tc, total; };
 struct BwdWs { size_t delta, gbuf, hsum, zsum, dhm, dzm, dwp, plans, lin, total; };
+struct DecayWs { size_t sums, rsums, total; };
 
 // Which backward kernels run: the tcgen05 attention backward for bf16
 // (unless SLA_FLAG_SIMT), and with it the tcgen05 linear-branch and
@@ -172,6 +173,38 @@ BwdWs bwd_ws(const Geom& g) {
   return w;
 }
 
+// Segments of the decayed linear attention: enough (head, segment) pairs for
+// two waves of one CTA per SM, whole chunks each.
+sla::DecayPlan decay_plan(const Geom& g) {
+  const int chunk = sla::decay_simt_chunk();
+  const int chunks = (g.N + chunk - 1) / chunk;
+  const int want = std::min(chunks, std::max(1, (2 * 148 + g.BH - 1) / g.BH));
+  sla::DecayPlan P;
+  P.N = g.N;
+  P.H = g.H;
+  P.seg_len = (chunks + want - 1) / want * chunk;
+  P.segs = (g.N + P.seg_len - 1) / P.seg_len;
+  return P;
+}
+
+DecayWs decay_ws(const Geom& g, bool backward) {
+  const sla::DecayPlan P = decay_plan(g);
+  const size_t states = P.segs > 1 ? sizeof(float) * size_t(g.BH) * P.segs * g.d * g.d : 0;
+  DecayWs w;
+  size_t off = kStatusBytes;
+  w.sums = off; off = align_up(off + states);
+  w.rsums = off; if (backward) off = align_up(off + states);
+  w.total = off;
+  return w;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 bool lists_ok(const sla_block_lists* l) {
   return l && l->crit_cnt && l->crit_idx && l->marg_cnt && l->marg_idx &&
          aligned16(l->crit_cnt) && aligned16(l->crit_idx) && aligned16(l->marg_cnt) &&
@@ -220,6 +253,8 @@ sla_status sla_workspace_size(const sla_params* p, int32_t op, size_t* bytes) {
     case SLA_OP_MASK: *bytes = mask_ws(g).total; return SLA_OK;
     case SLA_OP_FORWARD: *bytes = fwd_ws(g).total; return SLA_OK;
     case SLA_OP_BACKWARD: *bytes = bwd_ws(g).total; return SLA_OK;
+    case SLA_OP_DECAY: *bytes = decay_ws(g, false).total; return SLA_OK;
+    case SLA_OP_DECAY_BACKWARD: *bytes = decay_ws(g, true).total; return SLA_OK;
   }
   return SLA_ERR_INVALID_ARG;
 }
@@ -582,6 +617,272 @@ sla_status sla_permute_tokens(const sla_params* p, const void* src, void* dst, c
   if (a < b + bytes && b < a + bytes) return SLA_ERR_INVALID_ARG;  // overlapping
   SLA_CUDA(sla::launch_permute_rows(src, dst, perm, static_cast<sla::i64>(g.BH) * g.N, g.N, row_bytes,
                                     inverse != 0, static_cast<cudaStream_t>(stream)));
+  return SLA_OK;
+}
+
+// ---- rotary positions
+
+// Whether some row of d elements of a strided tensor meets some row of the
+// same tensor moved by `off` elements.  Dims from the largest stride down;
+// what the smaller dims cover is less than one step (the caller has checked
+// that), so only the two multiples around `off` can bring it near.
+static bool rows_meet(int64_t off, const int64_t* sr, const int64_t* size, const int* order, int dims,
+                      int64_t d) {
+  if (dims == 0) return off < d && -off < d;
+  const int i = *order;
+  if (size[i] == 1) return rows_meet(off, sr, size, order + 1, dims - 1, d);
+  int64_t m = off / sr[i] - (off % sr[i] < 0);
+  for (int c = 0; c < 2; ++c, ++m) {
+    const int64_t k = std::min(std::max(m, 1 - size[i]), size[i] - 1);
+    if (rows_meet(off - k * sr[i], sr, size, order + 1, dims - 1, d)) return true;
+  }
+  return false;
+}
+
+static bool rotary_pairs_ok(const sla_rotary* r) {
+  if (!r || r->rot_dim < 0 || r->rot_dim > 128 || (r->rot_dim & 1) || r->axes < 1 || r->axes > 3)
+    return false;
+  int64_t sum = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (r->axis_pairs[i] < 0 || (i >= r->axes && r->axis_pairs[i] != 0)) return false;
+    sum += r->axis_pairs[i];
+  }
+  return sum == r->rot_dim / 2;
+}
+
+sla_status sla_rotary_frequencies(sla_rotary* r, double base, int32_t scaling, double factor,
+                                  double trained_length, double beta_fast, double beta_slow) {
+  if (!rotary_pairs_ok(r)) return SLA_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !isfinite(base) || scaling < SLA_ROTARY_PLAIN || scaling > SLA_ROTARY_YARN)
+    return SLA_ERR_INVALID_ARG;
+  if (scaling != SLA_ROTARY_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return SLA_ERR_INVALID_ARG;
+  if (scaling == SLA_ROTARY_YARN &&
+      (!(trained_length > 0.0) || !isfinite(trained_length) || !(beta_slow > 0.0) ||
+       !(beta_fast > beta_slow) || !isfinite(beta_fast)))
+    return SLA_ERR_INVALID_ARG;
+  int at = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    const int P = r->axis_pairs[a];
+    double b = base;
+    if (scaling == SLA_ROTARY_NTK && P > 1) b = base * pow(factor, P / (P - 1.0));
+    // pair index at which a pair turns `beta` times over the trained length
+    auto corner = [&](double beta) {
+      return P * log(trained_length / (beta * 6.283185307179586477)) / log(base);
+    };
+    double lo = 0.0, hi = 1.0;
+    if (scaling == SLA_ROTARY_YARN) {
+      lo = std::max(floor(corner(beta_fast)), 0.0);
+      hi = std::min(ceil(corner(beta_slow)), 2.0 * P - 1.0);
+    }
+    for (int i = 0; i < P; ++i) {
+      double f = pow(b, -static_cast<double>(i) / P);
+      if (scaling == SLA_ROTARY_LINEAR) f /= factor;
+      if (scaling == SLA_ROTARY_YARN) {
+        const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+        f = f / factor * ramp + f * (1.0 - ramp);
+      }
+      r->freq[at++] = f;
+    }
+  }
+  for (; at < 64; ++at) r->freq[at] = 0.0;
+  r->amplitude = scaling == SLA_ROTARY_YARN ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
+  return SLA_OK;
+}
+
+sla_status sla_apply_rotary(const sla_params* p, const sla_rotary* r, const int64_t* raw_strides,
+                            void* q, void* k, void* q_rot, void* k_rot, int32_t rot_dtype,
+                            const int32_t* positions, int32_t pos_batched, const int32_t* perm,
+                            int32_t inverse, void* stream) {
+  Geom g;
+  sla_status st = make_geom(p, &g);
+  if (st != SLA_OK) return st;
+  if (!rotary_pairs_ok(r) || r->rot_dim > g.d || !isfinite(r->amplitude)) return SLA_ERR_INVALID_ARG;
+  if (r->layout != SLA_ROTARY_HALF && r->layout != SLA_ROTARY_INTERLEAVED) return SLA_ERR_INVALID_ARG;
+  for (int i = 0; i < r->rot_dim / 2; ++i)
+    if (!isfinite(r->freq[i])) return SLA_ERR_INVALID_ARG;
+  if (!tensor_ok(q) || !tensor_ok(q_rot) || (k == nullptr) != (k_rot == nullptr) ||
+      (k && (!aligned16(k) || !aligned16(k_rot))) || !aligned4(positions) || !aligned4(perm) ||
+      (inverse != 0 && inverse != 1) || (pos_batched != 0 && pos_batched != 1))
+    return SLA_ERR_INVALID_ARG;
+  if (rot_dtype != SLA_F32 && rot_dtype != g.dtype) return SLA_ERR_INVALID_ARG;
+  if (!positions && r->axes > 1 && r->rot_dim > 0) {
+    const int64_t F = r->axes == 3 ? r->grid[0] : 1, R = r->grid[r->axes - 2], C = r->grid[r->axes - 1];
+    if (F < 1 || R < 1 || C < 1 || R > g.N || C > g.N || F > g.N) return SLA_ERR_INVALID_ARG;
+    if ((r->axes == 3 ? F * R : R) * C != g.N) return SLA_ERR_INVALID_ARG;
+  }
+  // the raw side's strides, in elements
+  const int64_t dense[3] = {int64_t(g.H) * g.N * g.d, int64_t(g.N) * g.d, g.d};
+  int64_t sr[3];
+  const int unit = g.dtype == SLA_F32 ? 4 : 8;
+  const int64_t size[3] = {g.B, g.H, g.N};
+  int64_t span = g.d;  // elements from the first to behind the last
+  for (int i = 0; i < 3; ++i) {
+    sr[i] = size[i] == 1 ? 0 : raw_strides ? raw_strides[i] : dense[i];  // one: never stepped
+    if (sr[i] < 0 || sr[i] % unit || sr[i] > (int64_t(1) << 44)) return SLA_ERR_INVALID_ARG;
+    span += (size[i] - 1) * sr[i];
+    if (span > (int64_t(1) << 46)) return SLA_ERR_INVALID_ARG;
+  }
+  bool is_dense = true;  // extents of one have no stride to speak of
+  for (int i = 0; i < 3; ++i) is_dense = is_dense && (size[i] == 1 || sr[i] == dense[i]);
+  int order[3] = {0, 1, 2};  // largest stride first
+  std::sort(order, order + 3, [&](int a, int b) { return sr[a] > sr[b]; });
+  if (inverse) {
+    // written rows must not overlap: from the smallest stride up, each dim
+    // steps over all that the smaller ones cover
+    int64_t cover = g.d;
+    for (int x = 2; x >= 0; --x) {
+      const int i = order[x];
+      if (size[i] == 1) continue;
+      if (sr[i] < cover) return SLA_ERR_INVALID_ARG;
+      cover += (size[i] - 1) * sr[i];
+    }
+  }
+  const int esz = g.dtype == SLA_F32 ? 4 : 2, rsz = rot_dtype == SLA_F32 ? 4 : 2;
+  const uint64_t raw_bytes = uint64_t(span) * esz, rot_bytes = uint64_t(g.BH) * g.N * g.d * rsz;
+  void* raw[2] = {q, k};
+  void* rot[2] = {q_rot, k_rot};
+  const int tensors = k ? 2 : 1;
+  for (int i = 0; i < tensors; ++i)
+    for (int j = 0; j < tensors; ++j) {
+      const bool same = i == j && raw[i] == rot[j] && is_dense && esz == rsz && !perm;
+      if (!same && overlap(raw[i], raw_bytes, rot[j], rot_bytes)) return SLA_ERR_INVALID_ARG;
+    }
+  if (tensors == 2) {  // the two written tensors
+    if (!inverse && overlap(q_rot, rot_bytes, k_rot, rot_bytes)) return SLA_ERR_INVALID_ARG;
+    // two tensors side by side in one buffer (a fused projection's gradient)
+    // may lie between each other's rows
+    if (inverse && overlap(q, raw_bytes, k, raw_bytes)) {
+      const int64_t bytes = static_cast<char*>(k) - static_cast<char*>(q);
+      if (rows_meet(bytes / esz, sr, size, order, 3, g.d)) return SLA_ERR_INVALID_ARG;
+    }
+  }
+  const int32_t* pos = r->rot_dim > 0 ? positions : nullptr;
+  sla_rotary rr = *r;
+  if (r->axes == 2) { rr.grid[2] = r->grid[1]; rr.grid[1] = r->grid[0]; }
+  SLA_CUDA(sla::launch_rotary(g, rr, sr, raw, rot, tensors, rot_dtype == SLA_F32, pos, pos_batched != 0,
+                              perm, inverse != 0, static_cast<cudaStream_t>(stream)));
+  return SLA_OK;
+}
+
+// ---- linear attention with a decay for each head
+
+sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k, const void* v,
+                               const float* log_decay, const int32_t* lens, const float* state_in,
+                               void* out, float* state_out, void* ws, size_t ws_bytes,
+                               void* stream) {
+  Geom g;
+  sla_status st = make_geom(p, &g);
+  if (st != SLA_OK) return st;
+  if (!tensor_ok(q) || !tensor_ok(k) || !tensor_ok(v) || !tensor_ok(out) || !tensor_ok(ws) ||
+      !log_decay || !aligned4(log_decay) || !aligned4(lens) || !aligned16(state_in) ||
+      !aligned16(state_out))
+    return SLA_ERR_INVALID_ARG;
+  const uint64_t nx = uint64_t(g.BH) * g.N * g.d * (g.dtype == SLA_F32 ? 4 : 2);
+  const uint64_t ns = uint64_t(g.BH) * g.d * g.d * sizeof(float);
+  for (const void* x : {q, k, v})
+    if (overlap(out, nx, x, nx) || overlap(state_out, ns, x, nx)) return SLA_ERR_INVALID_ARG;
+  if (overlap(out, nx, state_in, ns) || overlap(out, nx, state_out, ns) ||
+      (state_in != state_out && overlap(state_in, ns, state_out, ns)))
+    return SLA_ERR_INVALID_ARG;
+  const DecayWs w = decay_ws(g, false);
+  if (ws_bytes < w.total) return SLA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t* status = at<int32_t>(ws, 0);
+  if (g.N <= SLA_DECAY_STEP_TOKENS) {
+    SLA_CUDA(sla::launch_decay_step(q, k, v, log_decay, lens, state_in, state_out, out, g, status, s));
+    return SLA_OK;
+  }
+  const sla::DecayPlan P = decay_plan(g);
+  const sla::DecayRole R{g.scale, g.scale, 1.0f, 0, false, false};
+  if (P.segs == 1) {
+    SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, state_in, int64_t(g.d) * g.d, out,
+                                        state_out, P, R, g, status, s));
+    return SLA_OK;
+  }
+  float* sums = at<float>(ws, w.sums);
+  SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
+  SLA_CUDA(sla::launch_decay_scan(sums, state_in, state_out, log_decay, lens, P, false, g, s));
+  SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, sums, int64_t(P.segs) * g.d * g.d, out,
+                                      nullptr, P, R, g, nullptr, s));
+  return SLA_OK;
+}
+
+sla_status sla_decay_attention_backward(const sla_params* p, const void* q, const void* k,
+                                        const void* v, const float* log_decay, const int32_t* lens,
+                                        const float* state_in, const void* dout,
+                                        const float* dstate_out, void* dq, void* dk, void* dv,
+                                        float* dstate_in, void* ws, size_t ws_bytes, void* stream) {
+  Geom g;
+  sla_status st = make_geom(p, &g);
+  if (st != SLA_OK) return st;
+  for (const void* x : {q, k, v, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                        static_cast<const void*>(dv), static_cast<const void*>(ws)})
+    if (!tensor_ok(x)) return SLA_ERR_INVALID_ARG;
+  if (!log_decay || !aligned4(log_decay) || !aligned4(lens) || !aligned16(state_in) ||
+      !aligned16(dstate_out) || !aligned16(dstate_in))
+    return SLA_ERR_INVALID_ARG;
+  const uint64_t nx = uint64_t(g.BH) * g.N * g.d * (g.dtype == SLA_F32 ? 4 : 2);
+  const uint64_t ns = uint64_t(g.BH) * g.d * g.d * sizeof(float);
+  const void* outs[] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* x : {q, k, v, dout})
+      if (overlap(outs[i], nx, x, nx) || overlap(dstate_in, ns, x, nx)) return SLA_ERR_INVALID_ARG;
+    for (const float* x : {state_in, dstate_out, static_cast<const float*>(dstate_in)})
+      if (overlap(outs[i], nx, x, ns)) return SLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], nx, outs[j], nx)) return SLA_ERR_INVALID_ARG;
+  }
+  if (overlap(dstate_in, ns, state_in, ns) ||
+      (dstate_in != dstate_out && overlap(dstate_in, ns, dstate_out, ns)))
+    return SLA_ERR_INVALID_ARG;
+  const DecayWs w = decay_ws(g, true);
+  if (ws_bytes < w.total) return SLA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t* status = at<int32_t>(ws, 0);
+  const sla::DecayPlan P = decay_plan(g);
+  const sla::DecayRole Rq{g.scale, g.scale, 1.0f, 0, false, true};
+  const sla::DecayRole Rv{g.scale, 1.0f, g.scale, 1, true, false};
+  const sla::DecayRole Rk{g.scale, 1.0f, g.scale, 1, true, true};
+  const int64_t one = int64_t(g.d) * g.d;
+  const float *s0 = state_in, *r0 = dstate_out;
+  int64_t stride = one;
+  float* fin = dstate_in;
+  if (P.segs > 1) {
+    float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
+    SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
+    SLA_CUDA(sla::launch_decay_scan(sums, state_in, nullptr, log_decay, lens, P, false, g, s));
+    SLA_CUDA(sla::launch_decay_sums_simt(q, dout, log_decay, lens, rsums, P, 1, true, g.scale, g, nullptr, s));
+    SLA_CUDA(sla::launch_decay_scan(rsums, dstate_out, dstate_in, log_decay, lens, P, true, g, s));
+    s0 = sums;
+    r0 = rsums;
+    stride = P.segs * one;
+    fin = nullptr;
+    status = nullptr;
+  }
+  SLA_CUDA(sla::launch_decay_out_simt(dout, v, k, log_decay, lens, s0, stride, dq, nullptr, P, Rq, g, status, s));
+  // dk before dv: with one segment the latter writes dstate_in, which may be dstate_out
+  SLA_CUDA(sla::launch_decay_out_simt(v, dout, q, log_decay, lens, r0, stride, dk, nullptr, P, Rk, g, nullptr, s));
+  SLA_CUDA(sla::launch_decay_out_simt(k, q, dout, log_decay, lens, r0, stride, dv, fin, P, Rv, g, nullptr, s));
+  return SLA_OK;
+}
+
+sla_status sla_decay_attention_step(const sla_params* p, const void* q, const void* k,
+                                    const void* v, const float* log_decay, const int32_t* lens,
+                                    float* state, void* out, void* stream) {
+  Geom g;
+  sla_status st = make_geom(p, &g);
+  if (st != SLA_OK) return st;
+  if (!tensor_ok(q) || !tensor_ok(k) || !tensor_ok(v) || !tensor_ok(out) || !tensor_ok(state) ||
+      !log_decay || !aligned4(log_decay) || !aligned4(lens))
+    return SLA_ERR_INVALID_ARG;
+  if (g.N > SLA_DECAY_STEP_TOKENS) return SLA_ERR_UNSUPPORTED;
+  const uint64_t nx = uint64_t(g.BH) * g.N * g.d * (g.dtype == SLA_F32 ? 4 : 2);
+  const uint64_t ns = uint64_t(g.BH) * g.d * g.d * sizeof(float);
+  for (const void* x : {q, k, v})
+    if (overlap(out, nx, x, nx) || overlap(state, ns, x, nx)) return SLA_ERR_INVALID_ARG;
+  if (overlap(out, nx, state, ns)) return SLA_ERR_INVALID_ARG;
+  SLA_CUDA(sla::launch_decay_step(q, k, v, log_decay, lens, state, state, out, g, nullptr,
+                                  static_cast<cudaStream_t>(stream)));
   return SLA_OK;
 }
 

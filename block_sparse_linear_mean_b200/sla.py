@@ -30,7 +30,10 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsla.so"
 SLA_OK, SLA_ERR_INVALID_ARG, SLA_ERR_UNSUPPORTED, SLA_ERR_WORKSPACE, SLA_ERR_CUDA, SLA_ERR_TIMEOUT = range(6)
 SLA_F32, SLA_BF16 = 0, 1
 SLA_MASK_TOPK, SLA_MASK_CDF = 0, 1
-SLA_OP_MASK, SLA_OP_FORWARD, SLA_OP_BACKWARD = 0, 1, 2
+SLA_OP_MASK, SLA_OP_FORWARD, SLA_OP_BACKWARD, SLA_OP_DECAY, SLA_OP_DECAY_BACKWARD = range(5)
+SLA_ROTARY_HALF, SLA_ROTARY_INTERLEAVED = 0, 1
+SLA_ROTARY_PLAIN, SLA_ROTARY_LINEAR, SLA_ROTARY_NTK, SLA_ROTARY_YARN = range(4)
+SLA_DECAY_STEP_TOKENS = 16
 SLA_FLAG_SIMT = 1
 SLA_FLAG_DEBUG_TIMEOUT = 2
 # SLA_DEBUG_WITHHOLD(kernel): which tensor-core kernel withholds a load under
@@ -54,6 +57,9 @@ EXPORTS = ("sla_abi_version", "sla_status_string", "sla_validate",
            "sla_backward", "sla_forward_uses_tensor_cores",
            "sla_block_importance", "sla_mask_recall",
            "sla_tile_order", "sla_permute_tokens",
+           "sla_rotary_frequencies", "sla_apply_rotary",
+           "sla_decay_attention", "sla_decay_attention_backward",
+           "sla_decay_attention_step",
            "sla_check_device_status")
 
 
@@ -69,6 +75,13 @@ class sla_params(ctypes.Structure):
 class sla_block_lists(ctypes.Structure):
     _fields_ = [("crit_cnt", ctypes.c_void_p), ("crit_idx", ctypes.c_void_p),
                 ("marg_cnt", ctypes.c_void_p), ("marg_idx", ctypes.c_void_p)]
+
+
+class sla_rotary(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("axis_pairs", ctypes.c_int32 * 3), ("grid", ctypes.c_int32 * 3),
+                ("origin", ctypes.c_int32 * 3), ("amplitude", ctypes.c_float),
+                ("freq", ctypes.c_double * 64)]
 
 
 class SlaError(RuntimeError):
@@ -137,6 +150,18 @@ def lib():
         L.sla_tile_order.argtypes = [I32, I32, I32, I32, I32, I32, VP, VP]
         L.sla_permute_tokens.restype = ctypes.c_int
         L.sla_permute_tokens.argtypes = [P(sla_params), VP, VP, VP, I32, I32, VP]
+        DBL = ctypes.c_double
+        L.sla_rotary_frequencies.restype = ctypes.c_int
+        L.sla_rotary_frequencies.argtypes = [P(sla_rotary), DBL, I32, DBL, DBL, DBL, DBL]
+        L.sla_apply_rotary.restype = ctypes.c_int
+        L.sla_apply_rotary.argtypes = [P(sla_params), P(sla_rotary), P(ctypes.c_int64), VP, VP, VP, VP,
+                                       I32, VP, I32, VP, I32, VP]
+        L.sla_decay_attention.restype = ctypes.c_int
+        L.sla_decay_attention.argtypes = [P(sla_params), VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+        L.sla_decay_attention_backward.restype = ctypes.c_int
+        L.sla_decay_attention_backward.argtypes = [P(sla_params)] + [VP] * 13 + [SZ, VP]
+        L.sla_decay_attention_step.restype = ctypes.c_int
+        L.sla_decay_attention_step.argtypes = [P(sla_params)] + [VP] * 8
         L.sla_check_device_status.restype = ctypes.c_int
         L.sla_check_device_status.argtypes = [VP, VP]
         _lib = L
@@ -244,6 +269,35 @@ def sla_tile_order(F, R, C, tf, tr, tc, perm, stream) -> int:
 
 def sla_permute_tokens(p, src, dst, perm, elem_bytes, inverse, stream) -> int:
     return lib().sla_permute_tokens(ctypes.byref(p), src, dst, perm, elem_bytes, inverse, stream)
+
+
+def sla_rotary_frequencies(r, base, scaling, factor, trained_length, beta_fast, beta_slow) -> int:
+    return lib().sla_rotary_frequencies(ctypes.byref(r), base, scaling, factor, trained_length,
+                                        beta_fast, beta_slow)
+
+
+def sla_apply_rotary(p, r, raw_strides, q, k, q_rot, k_rot, rot_dtype, positions, pos_batched, perm,
+                     inverse, stream) -> int:
+    """``raw_strides``: three ints (elements), or None for a dense raw side."""
+    rs = (ctypes.c_int64 * 3)(*raw_strides) if raw_strides is not None else None
+    return lib().sla_apply_rotary(ctypes.byref(p), ctypes.byref(r), rs, q, k, q_rot, k_rot, rot_dtype,
+                                  positions, pos_batched, perm, inverse, stream)
+
+
+def sla_decay_attention(p, q, k, v, log_decay, lens, state_in, out, state_out, ws, ws_bytes,
+                        stream) -> int:
+    return lib().sla_decay_attention(ctypes.byref(p), q, k, v, log_decay, lens, state_in, out,
+                                     state_out, ws, ws_bytes, stream)
+
+
+def sla_decay_attention_backward(p, q, k, v, log_decay, lens, state_in, dout, dstate_out, dq, dk, dv,
+                                 dstate_in, ws, ws_bytes, stream) -> int:
+    return lib().sla_decay_attention_backward(ctypes.byref(p), q, k, v, log_decay, lens, state_in, dout,
+                                              dstate_out, dq, dk, dv, dstate_in, ws, ws_bytes, stream)
+
+
+def sla_decay_attention_step(p, q, k, v, log_decay, lens, state, out, stream) -> int:
+    return lib().sla_decay_attention_step(ctypes.byref(p), q, k, v, log_decay, lens, state, out, stream)
 
 
 def sla_check_device_status(ws, stream) -> int:
@@ -483,6 +537,226 @@ def permute_tokens(p: sla_params, x: torch.Tensor, perm: torch.Tensor, inverse=F
     out = torch.empty_like(x)
     _check("sla_permute_tokens", sla_permute_tokens(p, x.data_ptr(), out.data_ptr(), perm.data_ptr(),
                                                     x.element_size(), 1 if inverse else 0, _stream()))
+    return out
+
+
+# ------------------------------------------------- rotary positions, decayed linear attention
+
+
+def token_params(B: int, H: int, N: int, d: int, dtype: torch.dtype, scale: float = 0.0,
+                 simt: bool = False) -> sla_params:
+    """Parameter block of the operators that take no block mask (rotary
+    positions, decayed linear attention, token moves): the mask fields hold
+    neutral values."""
+    return sla_params(B=B, H=H, N=N, d=d, block_q=128, block_k=128, dtype=_DTYPES[dtype],
+                      mask_mode=SLA_MASK_TOPK, scale=scale, flags=SLA_FLAG_SIMT if simt else 0)
+
+
+_DTYPES = {torch.float32: SLA_F32, torch.bfloat16: SLA_BF16}
+_TORCH_DTYPES = {SLA_F32: torch.float32, SLA_BF16: torch.bfloat16}
+
+
+def _enqueue(name, fn, p, args, device):
+    """Calls ``fn(p, *args, stream)`` on ``device``'s current stream."""
+    if device.index == torch.cuda.current_device():
+        st = fn(ctypes.byref(p), *args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(ctypes.byref(p), *args, torch.cuda.current_stream().cuda_stream)
+    if st != SLA_OK:
+        raise SlaError(name, st)
+
+
+def _want(t: torch.Tensor, name: str, shape, dtype, device, dense=True):
+    """Refuses a tensor that is not what the call is about to read."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: want {dtype} {list(shape)} on {device}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous tensor, got strides {t.stride()}")
+
+
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: want a CUDA tensor, got one on {t.device}")
+    return t.device
+
+
+def rotary(rot_dim: int, layout: str = "half", axis_pairs=None, grid=None, origin=(0, 0, 0),
+           scaling: str = "plain", factor: float = 1.0, base: float = 10000.0,
+           trained_length: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0) -> sla_rotary:
+    """Rotary positions of a model (``sla_rotary`` in sla.h), frequencies
+    filled in: ``layout`` "half" or "interleaved"; ``axis_pairs`` the pairs of
+    each axis (one axis by default); ``grid`` the latent grid that positions
+    are taken from when none are given; ``scaling`` "plain", "linear", "ntk"
+    or "yarn" by ``factor``."""
+    layouts = dict(half=SLA_ROTARY_HALF, interleaved=SLA_ROTARY_INTERLEAVED)
+    scalings = dict(plain=SLA_ROTARY_PLAIN, linear=SLA_ROTARY_LINEAR, ntk=SLA_ROTARY_NTK,
+                    yarn=SLA_ROTARY_YARN)
+    if layout not in layouts or scaling not in scalings:
+        raise ValueError(f"layout {layout!r}, scaling {scaling!r}: want one of {list(layouts)}, "
+                         f"{list(scalings)}")
+    pairs = [rot_dim // 2] if axis_pairs is None else list(axis_pairs)
+    if not 1 <= len(pairs) <= 3 or (grid is not None and len(grid) > 3) or len(origin) > 3:
+        raise ValueError("one to three axes")
+    r = sla_rotary(rot_dim=rot_dim, layout=layouts[layout], axes=len(pairs))
+    for i, x in enumerate(pairs):
+        r.axis_pairs[i] = x
+    for i, x in enumerate(grid or ()):
+        r.grid[i] = x
+    for i, x in enumerate(origin):
+        r.origin[i] = x
+    _check("sla_rotary_frequencies", sla_rotary_frequencies(r, base, scalings[scaling], factor,
+                                                            trained_length, beta_fast, beta_slow))
+    return r
+
+
+def _index(p, t, axes, device, name):
+    """(pointer, batched) of a positions tensor [axes, N] or [B, axes, N]
+    (the axes dim may be left out with one axis)."""
+    if t is None:
+        return None, 0
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous int32 on {device}")
+    shape = tuple(t.shape)
+    if shape == (axes, p.N) or (axes == 1 and shape == (p.N,)):
+        return t.data_ptr(), 0
+    if shape == (p.B, axes, p.N) or (axes == 1 and shape == (p.B, p.N)):
+        return t.data_ptr(), 1
+    raise ValueError(f"{name}: want [{axes}, {p.N}] or [{p.B}, {axes}, {p.N}], got {list(shape)}")
+
+
+def _rotary_call(p, r, raw, rot, positions, perm, inverse):
+    dev = _cuda(raw[0], "q")
+    shape = (p.B, p.H, p.N, p.d)
+    if len(raw) != len(rot) or not 1 <= len(raw) <= 2:
+        raise ValueError("one or two tensors on both sides")
+    strides = raw[0].stride()
+    for x, y in zip(raw, rot):
+        _want(x, "raw side", shape, _TORCH_DTYPES[p.dtype], dev, dense=False)
+        _want(y, "turned side", shape, rot[0].dtype, dev)
+        if x.stride(3) != 1 or any(a != b for n, a, b in zip(shape, x.stride(), strides) if n > 1):
+            raise ValueError("raw side: want both tensors with the same strides, channels adjacent")
+    if rot[0].dtype not in _DTYPES:
+        raise ValueError(f"turned side: {rot[0].dtype} is not supported")
+    pos, batched = _index(p, positions, r.axes, dev, "positions")
+    if perm is not None:
+        _want(perm, "perm", (p.N,), torch.int32, dev)
+    args = (ctypes.byref(r), (ctypes.c_int64 * 3)(*strides[:3]), raw[0].data_ptr(),
+            raw[1].data_ptr() if len(raw) > 1 else None, rot[0].data_ptr(),
+            rot[1].data_ptr() if len(rot) > 1 else None, _DTYPES[rot[0].dtype], pos, batched,
+            _ptr(perm), 1 if inverse else 0)
+    _enqueue("sla_apply_rotary", lib().sla_apply_rotary, p, args, dev)
+
+
+def apply_rotary(p: sla_params, r: sla_rotary, q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, perm: Optional[torch.Tensor] = None,
+                 out=None):
+    """q and k ``[B,H,N,d]`` (any strides with adjacent channels, the same for
+    both) turned by their tokens' positions, as dense ``[B,H,N,d]`` tensors in
+    the order ``perm``.  ``positions`` int32 ``[axes,N]`` or ``[B,axes,N]``
+    by raw token; without them ``r.grid`` and ``r.origin`` give them.  ``out``:
+    the tensors to write (q and k themselves are allowed when dense and no
+    order is given; fp32 is allowed for bf16 inputs)."""
+    raw = (q,) if k is None else (q, k)
+    if out is None:
+        rot = tuple(torch.empty(p.B, p.H, p.N, p.d, dtype=q.dtype, device=q.device) for _ in raw)
+    else:
+        rot = (out,) if torch.is_tensor(out) else tuple(out)
+    _rotary_call(p, r, raw, rot, positions, perm, False)
+    return rot[0] if k is None else rot
+
+
+def apply_rotary_backward(p: sla_params, r: sla_rotary, dq: torch.Tensor,
+                          dk: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                          perm: Optional[torch.Tensor] = None, out=None):
+    """Gradients of ``apply_rotary``'s inputs from those of its outputs (dense
+    ``[B,H,N,d]``, p's type or fp32), in p's type.  ``out``: the ``[B,H,N,d]``
+    tensors to write (any strides, the same for both); new ones lie as
+    ``[B,N,H,d]``, the projection's layout."""
+    rot = (dq,) if dk is None else (dq, dk)
+    if out is None:
+        raw = tuple(torch.empty(p.B, p.N, p.H, p.d, dtype=_TORCH_DTYPES[p.dtype],
+                                device=dq.device).transpose(1, 2) for _ in rot)
+    else:
+        raw = (out,) if torch.is_tensor(out) else tuple(out)
+    _rotary_call(p, r, raw, rot, positions, perm, True)
+    return raw[0] if dk is None else raw
+
+
+def _decay_inputs(p, tokens, log_decay, lens, states, ws=None):
+    dev = _cuda(tokens[0][1], tokens[0][0])
+    shape, dtype = (p.B, p.H, p.N, p.d), _TORCH_DTYPES[p.dtype]
+    for name, t in tokens:
+        _want(t, name, shape, dtype, dev)
+    _want(log_decay, "log_decay", (p.H,), torch.float32, dev)
+    if lens is not None:
+        _want(lens, "lens", (p.B,), torch.int32, dev)
+    for name, t in states:
+        if t is not None:
+            _want(t, name, (p.B, p.H, p.d, p.d), torch.float32, dev)
+    if ws is not None and (ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws: want contiguous uint8 on {dev} (sla.workspace)")
+    return dev
+
+
+def decay_attention(p: sla_params, q, k, v, log_decay: torch.Tensor,
+                    lens: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                    state_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> dict:
+    """Causal linear attention with a decay for each head
+    (``sla_decay_attention``): ``out`` and the state behind the last token.
+    ``state``: the state to go on from, ``[B,H,d,d]`` fp32; ``state_out`` may
+    be the same tensor."""
+    dev = _decay_inputs(p, (("q", q), ("k", k), ("v", v)), log_decay, lens,
+                        (("state", state), ("state_out", state_out)), ws)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, "out", q.shape, q.dtype, dev)
+    if state_out is None:
+        state_out = torch.empty(p.B, p.H, p.d, p.d, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = workspace(p, SLA_OP_DECAY, dev)
+    _enqueue("sla_decay_attention", lib().sla_decay_attention, p,
+             (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lens), _ptr(state),
+              out.data_ptr(), state_out.data_ptr(), ws.data_ptr(), ws.numel()), dev)
+    return dict(out=out, state=state_out, ws=ws)
+
+
+def decay_attention_backward(p: sla_params, q, k, v, log_decay: torch.Tensor, dout: torch.Tensor,
+                             lens: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                             dstate: Optional[torch.Tensor] = None,
+                             ws: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``decay_attention``: dq, dk, dv in p's type and the
+    gradient of the first state (fp32).  ``dstate``: the gradient that
+    reaches the state behind the last token."""
+    dev = _decay_inputs(p, (("q", q), ("k", k), ("v", v), ("dout", dout)), log_decay, lens,
+                        (("state", state), ("dstate", dstate)), ws)
+    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+    ds = torch.empty(p.B, p.H, p.d, p.d, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = workspace(p, SLA_OP_DECAY_BACKWARD, dev)
+    _enqueue("sla_decay_attention_backward", lib().sla_decay_attention_backward, p,
+             (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lens), _ptr(state),
+              dout.data_ptr(), _ptr(dstate), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+              ds.data_ptr(), ws.data_ptr(), ws.numel()), dev)
+    return dict(dq=dq, dk=dk, dv=dv, dstate=ds, ws=ws)
+
+
+def decay_attention_step(p: sla_params, q, k, v, log_decay: torch.Tensor, state: torch.Tensor,
+                         lens: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The newest ``p.N`` (at most 16) tokens of each sequence
+    (``sla_decay_attention_step``): returns ``out``, updates ``state`` in place."""
+    dev = _decay_inputs(p, (("q", q), ("k", k), ("v", v)), log_decay, lens, (("state", state),))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, "out", q.shape, q.dtype, dev)
+    _enqueue("sla_decay_attention_step", lib().sla_decay_attention_step, p,
+             (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lens),
+              state.data_ptr(), out.data_ptr()), dev)
     return out
 
 

@@ -34,7 +34,8 @@
  * - q, k, v, out and dout have the element type p->dtype (fp32 or bf16);
  *   everything else is fp32 or int32 as declared.  Gradients are fp32.
  * - All pointers except `stream` are DEVICE pointers, must be 16-byte aligned
- *   and are owned by the caller.  The library never allocates, frees or
+ *   and are owned by the caller, except where an argument is said to be a host
+ *   struct or to need less alignment (index arrays: 4 bytes).  The library never allocates, frees or
  *   synchronises (except sla_check_device_status), and keeps no state
  *   between calls.
  * - Every call only enqueues work on `stream` (a cudaStream_t; NULL = the
@@ -79,7 +80,13 @@ typedef enum {
   SLA_MASK_CDF = 1    /* keep the smallest top-ranked set with mass > 1 - thr */
 } sla_mask_mode;
 
-typedef enum { SLA_OP_MASK = 0, SLA_OP_FORWARD = 1, SLA_OP_BACKWARD = 2 } sla_op;
+typedef enum {
+  SLA_OP_MASK = 0,
+  SLA_OP_FORWARD = 1,
+  SLA_OP_BACKWARD = 2,
+  SLA_OP_DECAY = 3,           /* sla_decay_attention          */
+  SLA_OP_DECAY_BACKWARD = 4   /* sla_decay_attention_backward */
+} sla_op;
 
 /* Problem description.  Fractions are applied per query-block row; the count
  * is the smallest integer >= f * Nkb (with a 1e-9 slack against the binary
@@ -335,6 +342,126 @@ SLA_API sla_status sla_tile_order(int32_t F, int32_t R, int32_t C, int32_t tf, i
 SLA_API sla_status sla_permute_tokens(const sla_params* p, const void* src, void* dst,
                                       const int32_t* perm, int32_t elem_bytes, int32_t inverse,
                                       void* stream);
+
+/* Rotary positions: which channels of a head turn, by which angles.  Pair i of
+ * the rot_dim / 2 pairs at position x is turned by the angle x * freq[i]:
+ *   a' = amplitude (a cos - b sin),   b' = amplitude (b cos + a sin)
+ * where (a, b) are channels (i, i + rot_dim / 2) in the half layout and
+ * (2 i, 2 i + 1) in the interleaved one.  Channels rot_dim .. d - 1 are copied.
+ * With several axes (frame, row, column of a latent grid) the pairs are split
+ * among them in order, axis_pairs[0] to the first and so on.  A host struct,
+ * read during the call; sla_rotary_frequencies fills freq and amplitude, or
+ * the caller writes its own. */
+typedef enum { SLA_ROTARY_HALF = 0, SLA_ROTARY_INTERLEAVED = 1 } sla_rotary_layout;
+typedef struct {
+  int32_t rot_dim;        /* even, 0 .. d (0: nothing turns, a change of layout only) */
+  int32_t layout;         /* sla_rotary_layout                                        */
+  int32_t axes;           /* 1 .. 3                                                   */
+  int32_t axis_pairs[3];  /* >= 0, sum rot_dim / 2, zero beyond `axes`                */
+  int32_t grid[3];        /* positions NULL, several axes: grid[0] x grid[1] (x grid[2])
+                             tokens in raster order, N in all; unused with 1 axis      */
+  int32_t origin[3];      /* positions NULL: added to each axis' position             */
+  float amplitude;        /* factor on cos and sin, finite                            */
+  double freq[64];        /* radians per position, finite                             */
+} sla_rotary;
+
+/* How frequencies are stretched for sequences longer than the trained ones. */
+typedef enum {
+  SLA_ROTARY_PLAIN = 0,   /* freq = base^(-i / P) for pair i of an axis with P pairs   */
+  SLA_ROTARY_LINEAR = 1,  /* every frequency divided by `factor`                       */
+  SLA_ROTARY_NTK = 2,     /* base * factor^(P / (P - 1)): the slowest pair is stretched
+                             by `factor`, the fastest stays                            */
+  SLA_ROTARY_YARN = 3     /* pairs that turn less than beta_slow times over
+                             trained_length are divided by `factor`, those that turn
+                             more than beta_fast times stay, a linear ramp over the
+                             pair index between; amplitude = 0.1 ln(factor) + 1        */
+} sla_rotary_scaling;
+
+/* Fills r->freq and r->amplitude from r->rot_dim, axes and axis_pairs (each
+ * axis has the frequencies of a head of its own 2 * axis_pairs channels).
+ *   base > 1; factor >= 1 (not read for SLA_ROTARY_PLAIN); trained_length > 0,
+ *   beta_fast > beta_slow > 0 (read for SLA_ROTARY_YARN)
+ * Host only, in 64 bits. */
+SLA_API sla_status sla_rotary_frequencies(sla_rotary* r, double base, int32_t scaling,
+                                          double factor, double trained_length,
+                                          double beta_fast, double beta_slow);
+
+/* Turns q and k by their tokens' positions, or their gradients back.
+ *   q, k          the raw side: B x H x N rows of d channels of p->dtype, row
+ *                 (b, h, t) at element b * raw_strides[0] + h * raw_strides[1] +
+ *                 t * raw_strides[2] (a projection's [B, N, heads, d] output, say).
+ *                 k may be NULL with k_rot: one tensor only
+ *   raw_strides   3 host int64, multiples of 16 bytes; NULL: dense [B,H,N,d]
+ *   q_rot, k_rot  the turned side: dense [B,H,N,d] of rot_dtype (p->dtype or
+ *                 SLA_F32: sla_backward's gradients are fp32)
+ *   positions     [axes, N] int32, or [B, axes, N] with pos_batched = 1, by raw
+ *                 token; NULL: from r->grid and r->origin (token t itself, plus
+ *                 origin[0], with one axis)
+ *   perm          [N] int32 as for sla_permute_tokens, NULL: none.  Row n of
+ *                 the turned side is raw token perm[n].  Entries outside 0 .. N-1
+ *                 are skipped: nothing is read or written for them
+ *   inverse = 0:  x_rot[b, h, n, :] = R(t) x[b, h, t, :]
+ *   inverse = 1:  x[b, h, t, :] = R(t)^T x_rot[b, h, n, :]: the gradient of
+ *                 inverse = 0 (and its inverse where amplitude = 1)
+ * The angle is formed in 64 bits from position and frequency, so positions of
+ * any size keep their phase; the rotation is fp32, rounded once.  The written
+ * side may be the read side itself (same pointer, dense raw side of the same
+ * type, no perm); any other overlap is refused, and so are raw strides whose
+ * rows overlap where the raw side is written.  No workspace; asynchronous. */
+SLA_API sla_status sla_apply_rotary(const sla_params* p, const sla_rotary* r,
+                                    const int64_t* raw_strides, void* q, void* k, void* q_rot,
+                                    void* k_rot, int32_t rot_dtype, const int32_t* positions,
+                                    int32_t pos_batched, const int32_t* perm, int32_t inverse,
+                                    void* stream);
+
+/* Causal linear attention with a decay for each head.  With g = log_decay[h]
+ * and S the head's state, for each token in turn:
+ *   S <- e^g S + k_t v_t^T,     out_t = scale * q_t S
+ *   q, k, v    [B,H,N,d] dtype
+ *   log_decay  [H] fp32 device, natural logarithm of each head's decay, <= 0
+ *              (-infinity: a decay of zero); a constant of the model, it has no
+ *              gradient here
+ *   lens       [B] int32 device, nullable (N each): the first lens[b] tokens of
+ *              sequence b are real (clamped to 0 .. N); the rest, whatever it
+ *              holds, is not read into any result and its rows of `out` (of the
+ *              gradients, in the backward) are zero
+ *   state_in   [B,H,d,d] fp32, row = channel of k, column = channel of v
+ *              (nullable: zeros)
+ *   out        [B,H,N,d] dtype out
+ *   state_out  [B,H,d,d] fp32 out, nullable: the state behind each sequence's
+ *              last real token (state_in where it has none).  May be state_in
+ * bf16 runs on the tensor cores (SLA_FLAG_SIMT selects fp32 FMAs), fp32 on
+ * fp32 FMAs.  States are fp32 and keep fp32 accuracy.  p's block and mask
+ * fields are checked but not used.  Workspace: SLA_OP_DECAY; no output may
+ * overlap an input except state_out as said. */
+SLA_API sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k,
+                                       const void* v, const float* log_decay,
+                                       const int32_t* lens, const float* state_in, void* out,
+                                       float* state_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of sum(out * dout) + sum(state_out * dstate_out) of
+ * sla_decay_attention.
+ *   q, k, v, log_decay, lens, state_in  as given to the forward
+ *   dout         [B,H,N,d] dtype
+ *   dstate_out   [B,H,d,d] fp32, nullable (zeros)
+ *   dq, dk, dv   [B,H,N,d] dtype out (overwritten)
+ *   dstate_in    [B,H,d,d] fp32 out, nullable; may be dstate_out
+ * Nothing of the forward needs to be saved.  Workspace: SLA_OP_DECAY_BACKWARD. */
+SLA_API sla_status sla_decay_attention_backward(
+    const sla_params* p, const void* q, const void* k, const void* v, const float* log_decay,
+    const int32_t* lens, const float* state_in, const void* dout, const float* dstate_out,
+    void* dq, void* dk, void* dv, float* dstate_in, void* ws, size_t ws_bytes, void* stream);
+
+/* The same recurrence for the few newest tokens of each sequence: p->N = 1 ..
+ * SLA_DECAY_STEP_TOKENS tokens, one after another, the state read and written
+ * once.  q, k, v, out [B,H,N,d] dtype; `state` [B,H,d,d] fp32 is updated in
+ * place; lens as above (lens[b] = 0 leaves sequence b's state as it is).  fp32
+ * arithmetic for both types.  No workspace. */
+#define SLA_DECAY_STEP_TOKENS 16
+SLA_API sla_status sla_decay_attention_step(const sla_params* p, const void* q, const void* k,
+                                            const void* v, const float* log_decay,
+                                            const int32_t* lens, float* state, void* out,
+                                            void* stream);
 
 /* Synchronises `stream` and returns the status word the last call on `ws`
  * left (SLA_OK, or SLA_ERR_TIMEOUT when a bounded device-side wait gave up),

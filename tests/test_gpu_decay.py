@@ -1,0 +1,305 @@
+"""Linear attention with a decay for each head on the GPU, against the
+float64 oracle.
+
+Tolerances, from the roundings on the way (half a step of bf16 is 2^-8 of a
+value at most, of fp32 2^-24).  With M = the same sums over absolute values:
+* fp32 arithmetic: each sum of n terms is off by at most about n 2^-24 M; with
+  n <= a few hundred terms per chunk and product, 2^-15 M covers it (and the
+  decays' own 2^-20);
+* tensor cores: the weights of a chunk's pairs and the state are rounded to
+  bf16 once as operands, 2^-8 M each at most, so 2^-7 M together;
+* a bf16 result adds 2^-8 of its value.
+M is a worst case; the roundings are independent, so the error's 2-norm is
+also held to 3 * 2^-8 of the result's (one for each of the three roundings),
+and states, which are kept to fp32 accuracy, to 2^-17 of theirs."""
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_linear_mean_b200 import sla
+from gpu_util import to_np
+from oracle import token_ops as tok
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def randn(seed, *shape, dtype=F32):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def decays(H, kind="usual"):
+    if kind == "usual":
+        return torch.log1p(-torch.exp2(-torch.linspace(2, 10, H))).cuda()
+    return torch.tensor([[0.0, float("-inf"), -40.0, -1e-4][i % 4] for i in range(H)]).cuda()
+
+
+def near(got, want, mag, dtype, tc, what):
+    got, want = to_np(got), np.asarray(want)
+    assert np.isfinite(got).all(), what
+    tol = 2.0 ** -15 * mag + 1e-30
+    rel = 2.0 ** -17
+    if tc:
+        tol, rel = tol + 2.0 ** -7 * mag, 2 * 2.0 ** -8
+    if dtype == BF:
+        tol, rel = tol + 2.0 ** -8 * np.abs(want), rel + 2.0 ** -8
+    err = np.abs(got - want)
+    assert (err <= tol).all(), f"{what}: {np.max(err / tol):.3g} times the bound"
+    n = np.linalg.norm(want)
+    assert np.linalg.norm(got - want) <= rel * n + 1e-30, f"{what}: norm {np.linalg.norm(got - want) / n:.3g}"
+
+
+def state_near(got, want, mag, what):
+    got = to_np(got)
+    err = np.abs(got - want)
+    assert (err <= 2.0 ** -15 * mag + 1e-30).all(), f"{what}: {np.max(err / (2.0 ** -15 * mag + 1e-30)):.3g} times the bound"
+    n = np.linalg.norm(want)
+    assert np.linalg.norm(got - want) <= 2.0 ** -17 * n + 1e-30, f"{what}: norm {np.linalg.norm(got - want) / n:.3g}"
+
+
+CASES = [
+    # B, H, N, d, dtype, simt, lens, state, decays
+    (1, 1, 1, 64, F32, False, None, False, "usual"),
+    (1, 2, 16, 128, BF, False, None, True, "usual"),
+    (1, 2, 17, 64, F32, False, None, True, "usual"),
+    (1, 2, 17, 128, BF, False, None, True, "usual"),
+    (2, 3, 127, 128, BF, False, None, False, "usual"),
+    (2, 3, 128, 128, BF, False, None, True, "usual"),
+    (2, 3, 129, 128, BF, False, None, True, "usual"),
+    (1, 2, 300, 64, BF, False, None, True, "usual"),
+    (1, 2, 300, 128, BF, True, None, True, "usual"),
+    (1, 3, 1000, 64, F32, False, None, True, "usual"),
+    (1, 2, 1000, 128, F32, False, None, False, "usual"),
+    (1, 3, 1500, 128, BF, False, None, True, "usual"),
+    (2, 1, 2111, 64, BF, False, None, True, "usual"),
+    (4, 2, 500, 128, BF, False, [500, 0, 1, 257], True, "usual"),
+    (4, 2, 500, 64, BF, False, [128, 499, -3, 9999], True, "usual"),
+    (4, 2, 500, 64, F32, False, [0, 31, 33, 500], False, "usual"),
+    (3, 2, 20, 128, BF, False, [20, 0, 7], True, "usual"),
+    (3, 2, 12, 128, BF, False, [12, 0, 7], True, "usual"),
+    (1, 4, 700, 128, BF, False, None, True, "edge"),
+    (1, 4, 700, 64, F32, False, None, True, "edge"),
+    (1, 4, 700, 64, BF, False, None, True, "edge"),
+    (40, 4, 150, 128, BF, False, None, True, "usual"),   # more heads than SMs
+]
+
+
+def inputs(B, H, N, d, dtype, lens, state, kind):
+    q, k, v, do = (randn(i, B, H, N, d, dtype=dtype) for i in range(4))
+    s0, ds = (randn(4, B, H, d, d) * 3, randn(5, B, H, d, d)) if state else (None, None)
+    lt = None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
+    return q, k, v, do, s0, ds, lt, decays(H, kind)
+
+
+def magnitude(q, k, v, do, s0, ds, g, lens):
+    a = [np.abs(to_np(x)) for x in (q, k, v, do)]
+    s, r = (None if x is None else np.abs(to_np(x)) for x in (s0, ds))
+    fwd = tok.decay_forward(a[0], a[1], a[2], g.cpu(), lens, s)
+    bwd = tok.decay_backward(a[0], a[1], a[2], g.cpu(), a[3], lens, s, r)
+    return fwd, bwd
+
+
+def poison(lens, *tensors):
+    """NaN and infinity in the rows behind each sequence's end."""
+    if lens is not None:
+        for t in tensors:
+            for b, n in enumerate(lens):
+                t[b, :, max(n, 0)::2] = float("nan")
+                t[b, :, max(n, 0) + 1::2] = float("inf")
+
+
+@pytest.mark.parametrize("B,H,N,d,dtype,simt,lens,state,kind", CASES)
+def test_forward_and_backward(B, H, N, d, dtype, simt, lens, state, kind):
+    q, k, v, do, s0, ds, lt, g = inputs(B, H, N, d, dtype, lens, state, kind)
+    p = sla.token_params(B, H, N, d, dtype, simt=simt)
+    out, S = tok.decay_forward(q, k, v, g.cpu(), lens, s0)
+    grads = tok.decay_backward(q, k, v, g.cpu(), do, lens, s0, ds)
+    (mo, ms), mg = magnitude(q, k, v, do, s0, ds, g, lens)
+    poison(lens, q, k, v, do)
+    tc = dtype == BF and not simt
+    f = sla.decay_attention(p, q, k, v, g, lens=lt, state=s0)
+    b = sla.decay_attention_backward(p, q, k, v, g, do, lens=lt, state=s0, dstate=ds)
+    torch.cuda.synchronize()
+    assert sla.check_device_status(f["ws"]) == sla.SLA_OK
+    assert sla.check_device_status(b["ws"]) == sla.SLA_OK
+    near(f["out"], out, mo, dtype, tc, "out")
+    state_near(f["state"], S, ms, "state")
+    for name, want, mag in zip(("dq", "dk", "dv"), grads, mg):
+        near(b[name], want, mag, dtype, tc, name)
+    state_near(b["dstate"], grads[3], mg[3], "dstate")
+    if lens is not None:
+        for t in (f["out"], b["dq"], b["dk"], b["dv"]):
+            for i, n in enumerate(lens):
+                assert (t[i, :, max(n, 0):] == 0).all()
+
+
+def test_gradients_against_differences():
+    """The loss is linear in each argument alone: gradients against
+    differences of the library's own forward, in fp32."""
+    B, H, N, d = 1, 2, 200, 64
+    q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, F32, None, True, "usual")
+    p = sla.token_params(B, H, N, d, F32)
+    b = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds)
+
+    def loss(q, k, v, s0):
+        f = sla.decay_attention(p, q, k, v, g, state=s0)
+        return (f["out"].double() * do.double()).sum() + (f["state"].double() * ds.double()).sum()
+
+    for i, name in enumerate(("dq", "dk", "dv", "dstate")):
+        x = randn(20 + i, *(s0.shape if i == 3 else q.shape))
+        args = [q, k, v, s0]
+        up, dn = list(args), list(args)
+        up[i], dn[i] = args[i] + x / 2, args[i] - x / 2
+        # linear in each argument alone, so the step may be large: the
+        # difference is off by the forwards' roundings only
+        got = (loss(*up) - loss(*dn)).item()
+        want = (b[name].double() * x.double()).sum().item()
+        size = (b[name].double() * x.double()).abs().sum().item()
+        assert abs(got - want) <= 2.0 ** -12 * size, (name, got, want)
+
+
+@pytest.mark.parametrize("B,H,N,d,dtype,lens", [(1, 1, 1, 64, BF, None), (3, 5, 1, 128, F32, None),
+                                                (4, 3, 1, 128, BF, [1, 0, 1, -5]), (2, 2, 16, 64, F32, None),
+                                                (3, 2, 7, 128, BF, [7, 3, 0]), (64, 12, 1, 128, BF, None)])
+def test_step_against_oracle(B, H, N, d, dtype, lens):
+    q, k, v, do, s0, ds, lt, g = inputs(B, H, N, d, dtype, lens, True, "usual")
+    p = sla.token_params(B, H, N, d, dtype)
+    out, S = tok.decay_forward(q, k, v, g.cpu(), lens, s0)
+    (mo, ms), _ = magnitude(q, k, v, do, s0, ds, g, lens)
+    poison(lens, q, k, v)
+    state = s0.clone()
+    got = sla.decay_attention_step(p, q, k, v, g, state, lens=lt)
+    near(got, out, mo, dtype, False, "out")
+    state_near(state, S, ms, "state")
+    if lens is not None:
+        for i, n in enumerate(lens):
+            assert (got[i, :, max(n, 0):] == 0).all()
+            if n <= 0:
+                assert torch.equal(state[i], s0[i])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prompt_in_pieces_then_steps(dtype):
+    """A prompt in two pieces and four single tokens, the state carried in
+    place, gives what the whole sequence gives."""
+    B, H, N, d = 2, 3, 333, 128
+    q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, dtype, None, True, "usual")
+    out, S = tok.decay_forward(q, k, v, g.cpu(), None, s0)
+    (mo, ms), _ = magnitude(q, k, v, do, s0, ds, g, None)
+    state, got = s0.clone(), []
+    for a, b in ((0, 200), (200, 329)):
+        x = [t[:, :, a:b].contiguous() for t in (q, k, v)]
+        f = sla.decay_attention(sla.token_params(B, H, b - a, d, dtype), *x, g, state=state, state_out=state)
+        assert f["state"] is state
+        got.append(f["out"])
+    p1 = sla.token_params(B, H, 1, d, dtype)
+    for t in range(329, 333):
+        x = [y[:, :, t:t + 1].contiguous() for y in (q, k, v)]
+        got.append(sla.decay_attention_step(p1, *x, g, state))
+    near(torch.cat(got, 2), out, mo, dtype, dtype == BF, "out")
+    state_near(state, S, ms, "state")
+
+
+def test_rotary_then_prompt_then_gradients():
+    """q and k turned from a projection's layout, the decayed attention, its
+    gradients, and those turned back: the chain as a model runs it, against
+    the oracle on the library's own turned inputs."""
+    B, H, N, d = 2, 3, 260, 128
+    p, r = sla.token_params(B, H, N, d, BF), sla.rotary(d)
+    w, amp = tok.rotary_frequencies([d // 2])
+    qk = randn(30, B, N, 2, H, d, dtype=BF)
+    q, k = sla.apply_rotary(p, r, qk[:, :, 0].transpose(1, 2), qk[:, :, 1].transpose(1, 2))
+    v, do, g = randn(31, B, H, N, d, dtype=BF), randn(32, B, H, N, d, dtype=BF), decays(H)
+    f = sla.decay_attention(p, q, k, v, g)
+    b = sla.decay_attention_backward(p, q, k, v, g, do)
+    dq, dk = sla.apply_rotary_backward(p, r, b["dq"], b["dk"])
+    out, _ = tok.decay_forward(q, k, v, g.cpu())
+    grads = tok.decay_backward(q, k, v, g.cpu(), do)
+    (mo, _), mg = magnitude(q, k, v, do, None, None, g, None)
+    near(f["out"], out, mo, BF, True, "out")
+    pos = np.arange(N)[None]
+    for got, want, mag, name in ((dq, grads[0], mg[0], "dq"), (dk, grads[1], mg[1], "dk")):
+        # a turn keeps a pair's length, so its error is at most both channels' bounds
+        turned = tok.rotate(want, pos, [d // 2], w, amp, "half", inverse=True)
+        both = np.concatenate([mag[..., :d // 2] + mag[..., d // 2:]] * 2, -1)
+        tol = (2.0 ** -7 + 2.0 ** -15 + 2.0 ** -8) * both + 2.0 ** -8 * np.abs(turned)
+        err = np.abs(to_np(got) - turned)
+        assert (err <= tol).all(), name
+        assert np.linalg.norm(err) <= 4 * 2.0 ** -8 * np.linalg.norm(turned), name
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_workspace_reuse_in_place_state_and_graph(dtype):
+    B, H, N, d = 1, 3, 900, 128
+    q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, dtype, None, True, "usual")
+    p = sla.token_params(B, H, N, d, dtype)
+    want = sla.decay_attention(p, q, k, v, g, state=s0)
+    wb = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds)
+    # a workspace full of NaN, then its second use: results repeat bit for bit
+    ws = sla.workspace(p, sla.SLA_OP_DECAY_BACKWARD, "cuda").fill_(255)
+    for _ in range(2):
+        f = sla.decay_attention(p, q, k, v, g, state=s0, ws=ws)
+        b = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds, ws=ws)
+        assert torch.equal(f["out"], want["out"]) and torch.equal(f["state"], want["state"])
+        for n in ("dq", "dk", "dv", "dstate"):
+            assert torch.equal(b[n], wb[n])
+    # captured: forward with the state in place, replayed twice
+    state = s0.clone()
+    out = torch.empty_like(q)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        sla.decay_attention(p, q, k, v, g, state=state, state_out=state, out=out, ws=ws)
+        bg = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds, ws=ws)
+    state.copy_(s0)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want["out"]) and torch.equal(state, want["state"])
+    assert torch.equal(bg["dq"], wb["dq"]) and torch.equal(bg["dv"], wb["dv"])
+    gr.replay()
+    torch.cuda.synchronize()
+    second = sla.decay_attention(p, q, k, v, g, state=want["state"])
+    assert torch.equal(out, second["out"]) and torch.equal(state, second["state"])
+
+
+def test_other_stream():
+    B, H, N, d = 1, 2, 500, 128
+    q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, BF, None, True, "usual")
+    p = sla.token_params(B, H, N, d, BF)
+    want = sla.decay_attention(p, q, k, v, g, state=s0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = sla.decay_attention(p, q, k, v, g, state=s0)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got["out"], want["out"])
+
+
+def test_scale_is_applied():
+    B, H, N, d = 1, 2, 150, 128
+    q, k, v, do, _, _, _, g = inputs(B, H, N, d, BF, None, False, "usual")
+    p = sla.token_params(B, H, N, d, BF, scale=0.5)
+    out, _ = tok.decay_forward(q, k, v, g.cpu(), scale=0.5)
+    grads = tok.decay_backward(q, k, v, g.cpu(), do, scale=0.5)
+    f, b = sla.decay_attention(p, q, k, v, g), sla.decay_attention_backward(p, q, k, v, g, do)
+    for got, want in ((f["out"], out), (b["dq"], grads[0]), (b["dk"], grads[1]), (b["dv"], grads[2])):
+        assert np.linalg.norm(to_np(got) - want) <= 3 * 2.0 ** -8 * np.linalg.norm(want)
+
+
+def test_refusals():
+    p = sla.token_params(1, 2, 100, 64, BF)
+    x, g = randn(1, 1, 2, 100, 64, dtype=BF), decays(2)
+    for bad in ((x.float(), x, x, g), (x, x[:, :, ::2].repeat(1, 1, 2, 1).transpose(2, 3).contiguous().transpose(2, 3), x, g),
+                (x, x, x[:, :1], g), (x, x, x, g.double()), (x, x, x, g[:1]), (x, x, x, g.cpu())):
+        with pytest.raises(ValueError):
+            sla.decay_attention(p, *bad)
+    with pytest.raises(ValueError):
+        sla.decay_attention(p, x, x, x, g, lens=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        sla.decay_attention(p, x, x, x, g, state=torch.zeros(1, 2, 64, 64))
+    with pytest.raises(sla.SlaError):
+        sla.decay_attention(p, x, x, x, g, out=x)
+    with pytest.raises(sla.SlaError):
+        sla.decay_attention(p, x, x, x, g, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(sla.SlaError):
+        sla.decay_attention_step(p, x, x, x, g, torch.zeros(1, 2, 64, 64, device="cuda"))

@@ -1,0 +1,192 @@
+"""Rotary positions on the GPU against the float64 oracle.
+
+Tolerance: the rotation is two fp32 products and a sum of values |x| <= r
+(r^2 = a^2 + b^2) with cosines off by at most 2^-22 (a fraction of a turn
+rounded to 2^-25, and sincospif's own 2 ulp), so a result is off by at most
+2^-20 amplitude r; a bf16 result adds its rounding, 2^-8 of its value."""
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_linear_mean_b200 import sla
+from gpu_util import to_np
+from oracle import token_ops as tok
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def randn(seed, *shape, dtype=F32):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def radius(x, pairs, layout):
+    """Length of each channel's pair (of the channel itself where it is copied)."""
+    r = np.abs(x)
+    if layout == "half":
+        h = np.hypot(x[..., :pairs], x[..., pairs:2 * pairs])
+        r[..., :2 * pairs] = np.concatenate([h, h], -1)
+    else:
+        r[..., :2 * pairs] = np.repeat(np.hypot(x[..., 0:2 * pairs:2], x[..., 1:2 * pairs:2]), 2, -1)
+    return r
+
+
+def check(got, x, want, pairs, layout, amp, out_dtype, what):
+    tol = 2.0 ** -20 * max(amp, 1.0) * radius(to_np(x), pairs, layout) + 1e-30
+    if out_dtype == BF:
+        tol = tol + 2.0 ** -8 * np.abs(want) * 1.001
+    err = np.abs(to_np(got) - want)
+    assert (err <= tol).all(), f"{what}: {np.max(err / tol):.3g} times the bound"
+
+
+CASES = [
+    # B, H, N, d, dtype, rot_dim, layout, far
+    (1, 1, 1, 64, BF, 64, "half", 0),
+    (2, 3, 33, 128, BF, 128, "half", 10),
+    (2, 3, 33, 128, BF, 128, "interleaved", 1 << 20),
+    (1, 5, 257, 64, BF, 32, "half", 1 << 20),
+    (3, 2, 19, 128, F32, 128, "half", 1 << 20),
+    (3, 2, 19, 128, F32, 96, "interleaved", 500000),
+    (1, 2, 65, 64, BF, 42, "half", 99),          # 21 pairs: single elements
+    (1, 2, 65, 64, F32, 42, "interleaved", 99),
+    (1, 2, 65, 128, BF, 44, "half", 99),         # 22: pairs of elements
+    (1, 2, 65, 128, BF, 44, "interleaved", 99),
+    (1, 2, 65, 128, F32, 24, "half", 99),        # 12: fours
+    (1, 2, 65, 64, BF, 2, "half", 99),
+    (1, 2, 65, 64, BF, 0, "interleaved", 99),    # nothing turns
+    (24, 12, 1, 128, BF, 64, "half", 1 << 30),   # one token of each sequence
+    (1, 40, 130, 128, BF, 128, "interleaved", 7),
+]
+
+
+@pytest.mark.parametrize("B,H,N,d,dtype,rot,layout,far", CASES)
+def test_turn_and_back(B, H, N, d, dtype, rot, layout, far):
+    p = sla.token_params(B, H, N, d, dtype)
+    scaling = "yarn" if rot >= 64 else "ntk"
+    r = sla.rotary(rot, layout=layout, scaling=scaling, factor=4.0)
+    w, amp = tok.rotary_frequencies([rot // 2], scaling=scaling, factor=4.0)
+    amp = float(np.float32(amp))
+    qk = randn(1, B, N, 2, H, d, dtype=dtype)
+    q, k = qk[:, :, 0].transpose(1, 2), qk[:, :, 1].transpose(1, 2)
+    pos = torch.randint(0, far + 1, (B, 1, N), generator=torch.Generator().manual_seed(2),
+                        dtype=torch.int32).cuda()
+    got = sla.apply_rotary(p, r, q, k, positions=pos)
+    for x, y in zip((q, k), got):
+        assert y.is_contiguous()
+        check(y, x, tok.rotate(x, pos.cpu(), [rot // 2], w, amp, layout), rot // 2, layout, amp, dtype, "turned")
+    # gradients: fp32 and p's type, into a new tensor and into strided ones
+    for gt in {F32, dtype}:
+        dq, dk = randn(3, B, H, N, d, dtype=gt), randn(4, B, H, N, d, dtype=gt)
+        buf = torch.full((B, N, 2, H, d), float("nan"), dtype=dtype, device="cuda")
+        outs = buf[:, :, 0].transpose(1, 2), buf[:, :, 1].transpose(1, 2)
+        sla.apply_rotary_backward(p, r, dq, dk, positions=pos, out=outs)
+        alone = sla.apply_rotary_backward(p, r, dk, positions=pos)
+        assert alone.transpose(1, 2).is_contiguous() and torch.equal(alone, outs[1])
+        for x, y in zip((dq, dk), outs):
+            want = tok.rotate(x, pos.cpu(), [rot // 2], w, amp, layout, inverse=True)
+            check(y, x, want, rot // 2, layout, amp, dtype, f"gradient of {gt}")
+
+
+@pytest.mark.parametrize("grid,pairs,layout", [((3, 5, 7), (22, 21, 21), "interleaved"),
+                                               ((3, 5, 7), (8, 28, 28), "half"),
+                                               ((4, 9), (16, 16), "half"), ((1, 1, 1), (0, 32, 32), "half")])
+@pytest.mark.parametrize("tiled", [False, True])
+def test_grid_positions_and_order(grid, pairs, layout, tiled):
+    N, d, rot = int(np.prod(grid)), 128, 2 * sum(pairs)
+    origin = (11, 0, 3)[: len(grid)]
+    p = sla.token_params(1, 3, N, d, BF)
+    r = sla.rotary(rot, layout=layout, axis_pairs=pairs, grid=grid, origin=origin)
+    w, amp = tok.rotary_frequencies(pairs)
+    q = randn(5, 1, 3, N, d, dtype=BF)
+    perm = None
+    if tiled:
+        perm = torch.randperm(N, generator=torch.Generator().manual_seed(6)).to(torch.int32).cuda()
+    got = sla.apply_rotary(p, r, q, perm=perm)
+    pos = tok.grid_positions(grid, origin)
+    want = tok.rotate(q, pos, pairs, w, amp, layout)
+    order = np.arange(N) if perm is None else perm.cpu().numpy()
+    check(got, q[:, :, order], want[:, :, order], rot // 2, layout, 1.0, BF, "grid")
+    # the same positions given
+    given = sla.apply_rotary(p, r, q, positions=torch.from_numpy(pos.astype(np.int32)).cuda(), perm=perm)
+    assert torch.equal(got, given)
+    back = sla.apply_rotary_backward(p, r, got, perm=perm)
+    raw = np.empty((1, 3, N, d))
+    raw[:, :, order] = to_np(got)
+    check(back, torch.from_numpy(raw), tok.rotate(raw, pos, pairs, w, amp, layout, inverse=True), rot // 2,
+          layout, 1.0, BF, "grid back")
+
+
+@pytest.mark.parametrize("layout,rot", [("half", 64), ("half", 42), ("interleaved", 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_in_place_is_the_same(layout, rot, dtype):
+    B, H, N, d = 2, 3, 50, 128
+    p, r = sla.token_params(B, H, N, d, dtype), sla.rotary(rot, layout=layout)
+    q, k = randn(7, B, H, N, d, dtype=dtype), randn(8, B, H, N, d, dtype=dtype)
+    want = sla.apply_rotary(p, r, q, k)
+    back = sla.apply_rotary_backward(p, r, *want)
+    sla.apply_rotary(p, r, q, k, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    sla.apply_rotary_backward(p, r, q, k, out=(q, k))
+    assert torch.equal(q, back[0]) and torch.equal(k, back[1])
+
+
+def test_infinities_stay_in_their_pair_and_rows():
+    p, r = sla.token_params(1, 2, 9, 64, F32), sla.rotary(32)
+    q = randn(9, 1, 2, 9, 64)
+    clean = sla.apply_rotary(p, r, q)
+    q[0, 1, 4, 3], q[0, 0, 2, 40] = float("inf"), float("nan")
+    got = sla.apply_rotary(p, r, q)
+    same = (got == clean) | (got.isnan() & clean.isnan())
+    bad = (~same).nonzero().tolist()
+    assert bad == [[0, 0, 2, 40], [0, 1, 4, 3], [0, 1, 4, 19]]
+
+
+def test_entries_outside_an_order_are_skipped():
+    p, r = sla.token_params(1, 2, 6, 64, F32), sla.rotary(64)
+    q = randn(10, 1, 2, 6, 64)
+    out = torch.full_like(q, 7.0)
+    perm = torch.tensor([3, -1, 5, 6, 0, 2 ** 31 - 1], dtype=torch.int32).cuda()
+    sla.apply_rotary(p, r, q, perm=perm, out=out)
+    full = sla.apply_rotary(p, r, q)
+    for n, t in enumerate(perm.tolist()):
+        assert torch.equal(out[:, :, n], full[:, :, t] if 0 <= t < 6 else torch.full_like(q[:, :, 0], 7.0))
+
+
+def test_broadcast_input_and_wide_strides():
+    # every head reads one row (stride 0), rows with a gap behind them
+    B, H, N, d = 2, 4, 21, 64
+    p, r = sla.token_params(B, H, N, d, BF), sla.rotary(64)
+    base = randn(11, B, 1, N, d + 8, dtype=BF)
+    x = base[..., :d].expand(B, H, N, d)
+    assert torch.equal(sla.apply_rotary(p, r, x), sla.apply_rotary(p, r, x.contiguous()))
+
+
+def test_other_stream_and_graph():
+    B, H, N, d = 1, 4, 100, 128
+    p, r = sla.token_params(B, H, N, d, BF), sla.rotary(128)
+    q, out = randn(12, B, H, N, d, dtype=BF), torch.empty(B, H, N, d, dtype=BF, device="cuda")
+    want = sla.apply_rotary(p, r, q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sla.apply_rotary(p, r, q, out=out)
+    q.copy_(randn(13, B, H, N, d, dtype=BF))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, sla.apply_rotary(p, r, q)) and not torch.equal(out, want)
+
+
+def test_refusals():
+    p, r = sla.token_params(1, 2, 8, 64, BF), sla.rotary(64)
+    q = randn(14, 1, 2, 8, 64, dtype=BF)
+    for bad in (q.float(), q[:, :1], q[:, :, ::2].repeat(1, 1, 2, 1)[..., ::2]):
+        with pytest.raises(ValueError):
+            sla.apply_rotary(p, r, bad)
+    with pytest.raises(ValueError):
+        sla.apply_rotary(p, r, q, q.transpose(1, 2).contiguous().transpose(1, 2))  # other strides
+    with pytest.raises(ValueError):
+        sla.apply_rotary(p, r, q, positions=torch.zeros(7, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        sla.apply_rotary(p, r, q, positions=torch.zeros(8, dtype=torch.int64, device="cuda"))
+    with pytest.raises(sla.SlaError):
+        sla.apply_rotary(p, r, q, out=q[..., :].view(-1).view(1, 2, 8, 64), perm=torch.arange(8, dtype=torch.int32, device="cuda"))

@@ -1,0 +1,223 @@
+"""Host side of the token operators: frequencies against the oracle, struct
+layout, workspace sizes, and every refusal, before anything is enqueued (the
+addresses below are never dereferenced)."""
+
+import ctypes
+import math
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_linear_mean_b200 import sla, synth
+from block_sparse_linear_mean_b200.build import build
+from oracle import token_ops as tok
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 1 << 24            # aligned addresses, far apart
+ADDR = [A * (i + 1) for i in range(40)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build()
+    return sla.lib()
+
+
+def small(dtype=torch.bfloat16, B=2, H=3, N=40, d=64):
+    return sla.token_params(B, H, N, d, dtype)
+
+
+def test_rotary_struct_layout_matches_c_compiler(tmp_path):
+    src = tmp_path / "layout.c"
+    src.write_text(f'''#include <stdio.h>
+#include <stddef.h>
+#include "{ROOT}/include/sla.h"
+int main(void) {{
+  printf("%zu %zu %zu %zu %zu %zu %d %d %d\\n", sizeof(sla_rotary), offsetof(sla_rotary, axis_pairs),
+         offsetof(sla_rotary, grid), offsetof(sla_rotary, origin), offsetof(sla_rotary, amplitude),
+         offsetof(sla_rotary, freq), SLA_OP_DECAY, SLA_OP_DECAY_BACKWARD, SLA_DECAY_STEP_TOKENS);
+  return 0;
+}}
+''')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", str(src), "-o", str(exe)], check=True)
+    got = list(map(int, subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()))
+    R = sla.sla_rotary
+    assert got == [ctypes.sizeof(R), R.axis_pairs.offset, R.grid.offset, R.origin.offset,
+                   R.amplitude.offset, R.freq.offset, sla.SLA_OP_DECAY, sla.SLA_OP_DECAY_BACKWARD,
+                   sla.SLA_DECAY_STEP_TOKENS]
+
+
+@pytest.mark.parametrize("scaling,factor", [("plain", 1.0), ("linear", 4.0), ("ntk", 4.0), ("yarn", 16.0)])
+@pytest.mark.parametrize("pairs", [[64], [22, 21, 21], [1], [3, 0, 5], [21]])
+def test_frequencies_match_oracle(pairs, scaling, factor):
+    r = sla.rotary(2 * sum(pairs), axis_pairs=pairs, scaling=scaling, factor=factor, trained_length=2048)
+    w, amp = tok.rotary_frequencies(pairs, scaling=scaling, factor=factor, trained_length=2048)
+    np.testing.assert_allclose(list(r.freq)[:sum(pairs)], w, rtol=1e-14)
+    assert list(r.freq)[sum(pairs):] == [0.0] * (64 - sum(pairs))
+    assert r.amplitude == np.float32(amp)
+
+
+@pytest.mark.parametrize("kw", [dict(base=1.0), dict(base=math.inf), dict(base=math.nan),
+                                dict(scaling="linear", factor=0.5), dict(scaling="ntk", factor=math.nan),
+                                dict(scaling="yarn", factor=2.0, trained_length=0.0),
+                                dict(scaling="yarn", factor=2.0, beta_fast=1.0, beta_slow=1.0),
+                                dict(axis_pairs=[8, 9]), dict(axis_pairs=[17, -1])])
+def test_frequencies_refuse(kw):
+    with pytest.raises(sla.SlaError):
+        sla.rotary(32, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(layout="pairs"), dict(scaling="dynamic"), dict(axis_pairs=[4, 4, 4, 4])])
+def test_rotary_builder_refuses(kw):
+    with pytest.raises(ValueError):
+        sla.rotary(32, **kw)
+
+
+def rotary_call(p, r, strides=None, q=ADDR[0], k=ADDR[1], qr=ADDR[2], kr=ADDR[3], rot_dtype=sla.SLA_BF16,
+                pos=None, batched=0, perm=None, inverse=0):
+    return sla.sla_apply_rotary(p, r, strides, q, k, qr, kr, rot_dtype, pos, batched, perm, inverse, None)
+
+
+def test_apply_rotary_refuses():
+    p, r = small(), sla.rotary(64)
+    bad = sla.SLA_ERR_INVALID_ARG
+    assert rotary_call(p, r, q=None) == bad
+    assert rotary_call(p, r, qr=None) == bad
+    assert rotary_call(p, r, k=None) == bad                      # k without k_rot
+    assert rotary_call(p, r, q=ADDR[0] + 8) == bad
+    assert rotary_call(p, r, kr=ADDR[3] + 4) == bad
+    assert rotary_call(p, r, pos=ADDR[5] + 2) == bad
+    assert rotary_call(p, r, perm=ADDR[5] + 1) == bad
+    assert rotary_call(p, r, batched=2) == bad
+    assert rotary_call(p, r, inverse=2) == bad
+    assert rotary_call(p, r, rot_dtype=7) == bad
+    assert rotary_call(small(torch.float32), r, rot_dtype=sla.SLA_BF16) == bad
+    assert rotary_call(p, sla.rotary(128)) == bad                # more channels than the head has
+    for field, value in (("rot_dim", 63), ("rot_dim", -2), ("axes", 0), ("axes", 4), ("layout", 2),
+                         ("amplitude", math.inf)):
+        x = sla.rotary(64)
+        setattr(x, field, value)
+        assert rotary_call(p, x) == bad, field
+    x = sla.rotary(64)
+    x.freq[31] = math.nan
+    assert rotary_call(p, x) == bad
+    wrong = sla.token_params(1, 1, 8, 64, torch.float32)
+    wrong.d = 96
+    assert rotary_call(wrong, r) == sla.SLA_ERR_UNSUPPORTED
+
+
+def test_apply_rotary_refuses_strides_and_overlaps():
+    p, r = small(), sla.rotary(64)
+    bad = sla.SLA_ERR_INVALID_ARG
+    H, N, d = 3, 40, 64
+    assert rotary_call(p, r, strides=[H * N * d, N * d, d + 4]) == bad       # not 16 bytes
+    assert rotary_call(p, r, strides=[H * N * d, -N * d, d]) == bad
+    # in place: only dense, one type, no order
+    assert rotary_call(p, r, qr=ADDR[0], strides=[H * N * d, d, H * d]) == bad
+    assert rotary_call(p, r, qr=ADDR[0], rot_dtype=sla.SLA_F32) == bad
+    assert rotary_call(p, r, qr=ADDR[0], perm=ADDR[9]) == bad
+    assert rotary_call(p, r, qr=ADDR[0] + 128) == bad
+    assert rotary_call(p, r, kr=ADDR[2]) == bad                              # both into one
+    assert rotary_call(p, r, qr=ADDR[1]) == bad                              # q's result over k
+    # written rows that meet
+    assert rotary_call(p, r, inverse=1, strides=[0, N * d, d]) == bad
+    assert rotary_call(p, r, inverse=1, strides=[H * N * d, d, d]) == bad
+    assert rotary_call(p, r, inverse=1, strides=[N * H * d, d // 2, H * d]) == bad
+    # q and k in one buffer, k inside q's rows: half a row on, and one token on
+    tok_major = [N * 2 * H * d, d, 2 * H * d]
+    for off in (d // 2, d, 2 * H * d, 2 * H * d - d // 2, N * 2 * H * d):
+        assert rotary_call(p, r, inverse=1, strides=tok_major, k=ADDR[0] + 2 * off) == bad, off
+        assert rotary_call(p, r, inverse=1, strides=tok_major, q=ADDR[0] + 2 * off, k=ADDR[0]) == bad, off
+
+
+def test_apply_rotary_refuses_grids():
+    p = small(N=24)
+    bad = sla.SLA_ERR_INVALID_ARG
+    for grid in ((2, 3, 5), (0, 4, 6), (-2, -3, 4), (1 << 30, 1 << 30, 24)):
+        assert rotary_call(p, sla.rotary(64, axis_pairs=[12, 10, 10], grid=grid)) == bad
+    assert rotary_call(p, sla.rotary(64, axis_pairs=[12, 20], grid=(5, 5))) == bad
+
+
+def decay_args(**kw):
+    a = dict(q=ADDR[0], k=ADDR[1], v=ADDR[2], log_decay=ADDR[3], lens=None, state_in=None, out=ADDR[4],
+             state_out=None, ws=ADDR[5], ws_bytes=1 << 40)
+    a.update(kw)
+    return [a[x] for x in ("q", "k", "v", "log_decay", "lens", "state_in", "out", "state_out", "ws", "ws_bytes")]
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(k=ADDR[1] + 8), dict(v=None), dict(log_decay=None),
+                                dict(log_decay=ADDR[3] + 2), dict(lens=ADDR[8] + 1), dict(out=None),
+                                dict(state_in=ADDR[8] + 4), dict(state_out=ADDR[8] + 8), dict(ws=None),
+                                dict(out=ADDR[0]), dict(out=ADDR[2] + 256), dict(state_out=ADDR[1]),
+                                dict(state_out=ADDR[4]), dict(state_in=ADDR[4]),
+                                dict(state_in=ADDR[8], state_out=ADDR[8] + 4096)])
+def test_decay_attention_refuses(kw):
+    assert sla.sla_decay_attention(small(), *decay_args(**kw), None) == sla.SLA_ERR_INVALID_ARG
+
+
+def test_decay_attention_refuses_small_workspace_and_bad_params():
+    p = small(N=4000)
+    need = sla.sla_workspace_size(p, sla.SLA_OP_DECAY)
+    assert sla.sla_decay_attention(p, *decay_args(ws_bytes=need - 1), None) == sla.SLA_ERR_WORKSPACE
+    p.d = 80
+    assert sla.sla_decay_attention(p, *decay_args(), None) == sla.SLA_ERR_UNSUPPORTED
+
+
+def back_args(**kw):
+    a = dict(q=ADDR[0], k=ADDR[1], v=ADDR[2], log_decay=ADDR[3], lens=None, state_in=None, dout=ADDR[4],
+             dstate_out=None, dq=ADDR[5], dk=ADDR[6], dv=ADDR[7], dstate_in=None, ws=ADDR[9],
+             ws_bytes=1 << 40)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [dict(dout=None), dict(dq=None), dict(dk=ADDR[6] + 2), dict(dv=ADDR[0]),
+                                dict(dk=ADDR[5]), dict(dq=ADDR[4]), dict(log_decay=None), dict(ws=None),
+                                dict(dstate_in=ADDR[7]), dict(state_in=ADDR[8], dstate_in=ADDR[8]),
+                                dict(dstate_out=ADDR[8], dstate_in=ADDR[8] + 64), dict(lens=ADDR[8] + 3),
+                                dict(dstate_out=ADDR[6])])
+def test_decay_backward_refuses(kw):
+    assert sla.sla_decay_attention_backward(small(), *back_args(**kw), None) == sla.SLA_ERR_INVALID_ARG
+
+
+def test_decay_backward_refuses_small_workspace():
+    p = small(N=4000)
+    need = sla.sla_workspace_size(p, sla.SLA_OP_DECAY_BACKWARD)
+    assert sla.sla_decay_attention_backward(p, *back_args(ws_bytes=need - 1), None) == sla.SLA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("kw,want", [(dict(q=None), 1), (dict(state=None), 1), (dict(state=ADDR[0]), 1),
+                                     (dict(out=ADDR[2]), 1), (dict(out=ADDR[5]), 1), (dict(lens=ADDR[8] + 2), 1),
+                                     (dict(log_decay=None), 1)])
+def test_decay_step_refuses(kw, want):
+    a = dict(q=ADDR[0], k=ADDR[1], v=ADDR[2], log_decay=ADDR[3], lens=None, state=ADDR[5], out=ADDR[4])
+    a.update(kw)
+    assert sla.sla_decay_attention_step(small(N=1), *a.values(), None) == want
+
+
+def test_decay_step_refuses_many_tokens():
+    assert sla.sla_decay_attention_step(small(N=17), *ADDR[:4], None, ADDR[5], ADDR[6],
+                                        None) == sla.SLA_ERR_UNSUPPORTED
+
+
+def test_workspaces_of_every_workload():
+    for wl in synth.WORKLOADS.values():
+        p = sla.params_for(wl)
+        for op in (sla.SLA_OP_DECAY, sla.SLA_OP_DECAY_BACKWARD):
+            n = sla.sla_workspace_size(p, op)
+            assert n >= 256 and n % 256 == 0 and n < 1 << 30
+
+
+def test_tensor_helpers_refuse_cpu_tensors():
+    p = small()
+    x = torch.zeros(2, 3, 40, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        sla.apply_rotary(p, sla.rotary(64), x, x)
+    with pytest.raises(ValueError):
+        sla.decay_attention(p, x, x, x, torch.zeros(3))
+    with pytest.raises(ValueError):
+        sla.decay_attention_step(p, x, x, x, torch.zeros(3), torch.zeros(2, 3, 64, 64))
