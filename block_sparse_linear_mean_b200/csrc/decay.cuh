@@ -8,13 +8,28 @@
 namespace sla {
 
 #ifdef __CUDACC__
-// decay^n = 2^(n l2), l2 = log2 of the head's decay (-inf for a decay of
-// zero).  The product's rounding is 2^-24 of the exponent: a weight that
-// matters (2^-20 and up) is off by at most 20 * 2^-24 * ln 2, under 2^-20.
-__device__ __forceinline__ float decay_log2(float log_decay) { return log_decay * 1.4426950408889634f; }
-__device__ __forceinline__ float decay_power(float l2, int n) {
-  return n == 0 ? 1.f : exp2f(static_cast<float>(n) * l2);
+// decay^n = 2^(n log2 e log_decay); -inf is a decay of zero.  The exponent is
+// formed and reduced in 64 bits: in 32 its rounding alone would put powers of
+// a few hundred tokens off by 2^-20, the same way for every element.
+__device__ __forceinline__ double decay_log2(float log_decay) {
+  return static_cast<double>(log_decay) * 1.4426950408889634074;
 }
+__device__ __forceinline__ float decay_power(double l2, int n) {
+  if (n == 0) return 1.f;
+  const double x = fmax(static_cast<double>(n) * l2, -1e6);
+  const double i = rint(x);
+  return ldexpf(exp2f(static_cast<float>(x - i)), static_cast<int>(i));
+}
+// The same as an unevaluated sum of two floats, for factors that are applied
+// again and again (a chunk's, a segment's): their error grows with the number
+// of times.
+__device__ __forceinline__ float2 decay_power2(double l2, int n) {
+  if (n == 0) return make_float2(1.f, 0.f);
+  const double p = exp2(static_cast<double>(n) * l2);
+  const float hi = static_cast<float>(p);
+  return make_float2(hi, static_cast<float>(p - static_cast<double>(hi)));
+}
+__device__ __forceinline__ float times(float2 f, float s) { return fmaf(f.x, s, f.y * s); }
 
 // Real tokens of sequence b, and of its segment `seg`.
 __device__ __forceinline__ int sequence_tokens(const DecayPlan& P, const int32_t* lens, int b) {

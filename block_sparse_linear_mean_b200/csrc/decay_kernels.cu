@@ -52,7 +52,7 @@ __device__ __forceinline__ void load_rows(const T* __restrict__ x, float* dst, i
 // each thread owns D * D / 256 elements: rows ty + 16 x, columns 4 tx + 64 y
 template <int D>
 __device__ __forceinline__ void add_outer(float* S, const float* b, const float* c, const float* w,
-                                          float f) {
+                                          float2 f) {
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   constexpr int LD = D + 4, RX = D / 16, CY = D / 64;
   float acc[RX][CY * 4];
@@ -61,8 +61,8 @@ __device__ __forceinline__ void add_outer(float* S, const float* b, const float*
 #pragma unroll
     for (int y = 0; y < CY; ++y) {
       const float4 s = *reinterpret_cast<const float4*>(S + (ty + 16 * x) * LD + 4 * tx + 64 * y);
-      acc[x][4 * y] = f * s.x; acc[x][4 * y + 1] = f * s.y;
-      acc[x][4 * y + 2] = f * s.z; acc[x][4 * y + 3] = f * s.w;
+      acc[x][4 * y] = times(f, s.x); acc[x][4 * y + 1] = times(f, s.y);
+      acc[x][4 * y + 2] = times(f, s.z); acc[x][4 * y + 3] = times(f, s.w);
     }
 #pragma unroll 2
   for (int r = 0; r < kC; ++r) {
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThr) decay_sums_simt(const T* __restrict__ b,
   float* ct = bt + kC * (D + 4);
   __shared__ float w[kC];
   const int bh = blockIdx.y, seg = blockIdx.x;
-  const float l2 = decay_log2(log_decay[bh % P.H]);
+  const double l2 = decay_log2(log_decay[bh % P.H]);
   const int t0 = seg * P.seg_len, n = segment_tokens(P, lens, bh / P.H, seg);
   const i64 base = i64(bh) * P.N * D;
   load_state<D>(S, nullptr, false);
@@ -119,11 +119,13 @@ __global__ void __launch_bounds__(kThr) decay_sums_simt(const T* __restrict__ b,
     __syncthreads();
     load_rows<T, D>(b + base, bt, i0, n, t0, reverse);
     load_rows<T, D>(c + base, ct, i0, n, t0, reverse);
-    const int nc = min(kC, n - i0);
-    if (threadIdx.x < kC)
-      w[threadIdx.x] = threadIdx.x < nc ? w_sum * decay_power(l2, nc - 1 - threadIdx.x + e) : 0.f;
+    // weights count from the segment's end: nothing is scaled again later
+    if (threadIdx.x < kC) {
+      const int left = n - 1 - i0 - static_cast<int>(threadIdx.x);
+      w[threadIdx.x] = left >= 0 ? w_sum * decay_power(l2, left + e) : 0.f;
+    }
     __syncthreads();
-    add_outer<D>(S, bt, ct, w, decay_power(l2, nc));
+    add_outer<D>(S, bt, ct, w, make_float2(1.f, 0.f));
   }
   __syncthreads();
   float* dst = sums + (i64(bh) * P.segs + seg) * D * D;
@@ -149,11 +151,12 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
   float* pt = ct + kC * LD;  // [kC][kC + 1]
   __shared__ float w[kC], pw[kC + 1];
   const int bh = blockIdx.y, seg = blockIdx.x;
-  const float l2 = decay_log2(log_decay[bh % P.H]);
+  const double l2 = decay_log2(log_decay[bh % P.H]);
   const int t0 = seg * P.seg_len, n = segment_tokens(P, lens, bh / P.H, seg);
   const i64 base = i64(bh) * P.N * D;
   load_state<D>(S, starts ? starts + i64(bh) * start_stride + i64(seg) * D * D : nullptr, R.transposed);
   if (threadIdx.x <= kC) pw[threadIdx.x] = decay_power(l2, threadIdx.x);
+  const float2 full = decay_power2(l2, kC);
   for (int i0 = 0; i0 < n; i0 += kC) {
     __syncthreads();
     load_rows<T, D>(a + base, at, i0, n, t0, R.reverse);
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
       }
     }
     __syncthreads();
-    add_outer<D>(S, bt, ct, w, pw[nc]);
+    add_outer<D>(S, bt, ct, w, nc == kC ? full : decay_power2(l2, nc));
   }
   // rows behind the sequence's end
   const int pad = min(P.seg_len, P.N - t0) - n;
@@ -249,11 +252,11 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(float4* __restrict__ su
   const int u = blockIdx.x * 256 + threadIdx.x;
   const int bh = blockIdx.y;
   if (u >= dd4) return;
-  const float l2 = decay_log2(log_decay[bh % P.H]);
+  const double l2 = decay_log2(log_decay[bh % P.H]);
   const int len = sequence_tokens(P, lens, bh / P.H);
   float4 s = first ? first[i64(bh) * dd4 + u] : make_float4(0.f, 0.f, 0.f, 0.f);
   float4* row = sums + i64(bh) * P.segs * dd4 + u;
-  const float full = decay_power(l2, P.seg_len);
+  const float2 full = decay_power2(l2, P.seg_len);
   for (int i0 = 0; i0 < P.segs; i0 += 8) {
     float4 x[8];
 #pragma unroll
@@ -267,9 +270,9 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(float4* __restrict__ su
         const int seg = reverse ? P.segs - 1 - (i0 + i) : i0 + i;
         row[i64(seg) * dd4] = s;
         const int n = min(max(len - seg * P.seg_len, 0), P.seg_len);
-        const float f = n == P.seg_len ? full : decay_power(l2, n);
-        s.x = fmaf(f, s.x, x[i].x); s.y = fmaf(f, s.y, x[i].y);
-        s.z = fmaf(f, s.z, x[i].z); s.w = fmaf(f, s.w, x[i].w);
+        const float2 f = n == P.seg_len ? full : decay_power2(l2, n);
+        s.x = fmaf(f.x, s.x, fmaf(f.y, s.x, x[i].x)); s.y = fmaf(f.x, s.y, fmaf(f.y, s.y, x[i].y));
+        s.z = fmaf(f.x, s.z, fmaf(f.y, s.z, x[i].z)); s.w = fmaf(f.x, s.w, fmaf(f.y, s.w, x[i].w));
       }
     }
   }

@@ -263,6 +263,23 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
                                   const int32_t* lens, const float* starts, i64 start_stride, void* out,
                                   float* final_state, const DecayPlan& P, const DecayRole& R,
                                   const Geom& g, int32_t* zero, cudaStream_t s);
+// on the tensor cores (decay_tc.cu); a launch sums one or two jobs
+bool decay_tc_supported(const Geom& g);
+int decay_tc_chunk();
+struct DecaySums {
+  const void *b, *c;
+  float* sums;
+  float w_sum;
+  int e;
+  bool reverse;
+};
+cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* log_decay,
+                                 const int32_t* lens, const DecayPlan& P, const Geom& g,
+                                 int32_t* status, int32_t* zero, cudaStream_t s);
+cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, const float* log_decay,
+                                const int32_t* lens, const float* starts, i64 start_stride, void* out,
+                                const DecayPlan& P, const DecayRole& R, const Geom& g, int32_t* status,
+                                int32_t* zero, cudaStream_t s);
 cudaError_t launch_decay_scan(float* sums, const float* first, float* final_state,
                               const float* log_decay, const int32_t* lens, const DecayPlan& P,
                               bool reverse, const Geom& g, cudaStream_t s);

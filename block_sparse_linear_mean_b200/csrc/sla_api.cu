@@ -176,7 +176,7 @@ BwdWs bwd_ws(const Geom& g) {
 // Segments of the decayed linear attention: enough (head, segment) pairs for
 // two waves of one CTA per SM, whole chunks each.
 sla::DecayPlan decay_plan(const Geom& g) {
-  const int chunk = sla::decay_simt_chunk();
+  const int chunk = sla::decay_tc_supported(g) ? sla::decay_tc_chunk() : sla::decay_simt_chunk();
   const int chunks = (g.N + chunk - 1) / chunk;
   const int want = std::min(chunks, std::max(1, (2 * 148 + g.BH - 1) / g.BH));
   sla::DecayPlan P;
@@ -189,7 +189,8 @@ sla::DecayPlan decay_plan(const Geom& g) {
 
 DecayWs decay_ws(const Geom& g, bool backward) {
   const sla::DecayPlan P = decay_plan(g);
-  const size_t states = P.segs > 1 ? sizeof(float) * size_t(g.BH) * P.segs * g.d * g.d : 0;
+  const bool sums = P.segs > 1 || sla::decay_tc_supported(g);
+  const size_t states = sums ? sizeof(float) * size_t(g.BH) * P.segs * g.d * g.d : 0;
   DecayWs w;
   size_t off = kStatusBytes;
   w.sums = off; off = align_up(off + states);
@@ -794,6 +795,24 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
   }
   const sla::DecayPlan P = decay_plan(g);
   const sla::DecayRole R{g.scale, g.scale, 1.0f, 0, false, false};
+  if (sla::decay_tc_supported(g)) {
+    // the state that is handed on comes from the sums kernel, which keeps it
+    // to fp32 accuracy; one segment and no state wanted need no sums
+    float* sums = at<float>(ws, w.sums);
+    const float* starts = state_in;
+    int64_t stride = int64_t(g.d) * g.d;
+    int32_t* zero = status;
+    if (P.segs > 1 || state_out) {
+      const sla::DecaySums job{k, v, sums, 1.0f, 0, false};
+      SLA_CUDA(sla::launch_decay_sums_tc(&job, 1, log_decay, lens, P, g, status, zero, s));
+      SLA_CUDA(sla::launch_decay_scan(sums, state_in, state_out, log_decay, lens, P, false, g, s));
+      starts = sums;
+      stride *= P.segs;
+      zero = nullptr;
+    }
+    SLA_CUDA(sla::launch_decay_out_tc(q, k, v, log_decay, lens, starts, stride, out, P, R, g, status, zero, s));
+    return SLA_OK;
+  }
   if (P.segs == 1) {
     SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, state_in, int64_t(g.d) * g.d, out,
                                         state_out, P, R, g, status, s));
@@ -847,6 +866,29 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
   const float *s0 = state_in, *r0 = dstate_out;
   int64_t stride = one;
   float* fin = dstate_in;
+  if (sla::decay_tc_supported(g)) {
+    float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
+    int32_t* zero = status;
+    int64_t rstride = one;
+    const sla::DecaySums jobs[2] = {{q, dout, rsums, g.scale, 1, true}, {k, v, sums, 1.0f, 0, false}};
+    const bool need_s = P.segs > 1, need_r = P.segs > 1 || dstate_in;
+    if (need_r) {
+      SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, P, g, status, zero, s));
+      SLA_CUDA(sla::launch_decay_scan(rsums, dstate_out, dstate_in, log_decay, lens, P, true, g, s));
+      r0 = rsums;
+      rstride = P.segs * one;
+      zero = nullptr;
+    }
+    if (need_s) {
+      SLA_CUDA(sla::launch_decay_scan(sums, state_in, nullptr, log_decay, lens, P, false, g, s));
+      s0 = sums;
+      stride = P.segs * one;
+    }
+    SLA_CUDA(sla::launch_decay_out_tc(dout, v, k, log_decay, lens, s0, stride, dq, P, Rq, g, status, zero, s));
+    SLA_CUDA(sla::launch_decay_out_tc(v, dout, q, log_decay, lens, r0, rstride, dk, P, Rk, g, status, nullptr, s));
+    SLA_CUDA(sla::launch_decay_out_tc(k, q, dout, log_decay, lens, r0, rstride, dv, P, Rv, g, status, nullptr, s));
+    return SLA_OK;
+  }
   if (P.segs > 1) {
     float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
     SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
