@@ -31,12 +31,13 @@ __device__ __forceinline__ float2 decay_power2(double l2, int n) {
 }
 __device__ __forceinline__ float times(float2 f, float s) { return fmaf(f.x, s, f.y * s); }
 
-// Real tokens of sequence b, and of its segment `seg`.
-__device__ __forceinline__ int sequence_tokens(const DecayPlan& P, const int32_t* lens, int b) {
-  return lens ? min(max(lens[b], 0), P.N) : P.N;
+// Real tokens of sequence b.
+__device__ __forceinline__ int decay_tokens(const int32_t* lens, int b, int N) {
+  return lens ? min(max(lens[b], 0), N) : N;
 }
+// Those of segment `seg` of the fp32 kernels.
 __device__ __forceinline__ int segment_tokens(const DecayPlan& P, const int32_t* lens, int b, int seg) {
-  return min(max(sequence_tokens(P, lens, b) - seg * P.seg_len, 0), P.seg_len);
+  return min(max(decay_tokens(lens, b, P.N) - seg * P.seg_len, 0), P.seg_len);
 }
 #endif
 

@@ -240,43 +240,83 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
   }
 }
 
-// (2) sums[bh][seg] -> the state at the segment's start (in the direction of
-// the walk), in place; the state behind the last segment -> final_state.
-// One thread per 4 elements, segments in order: sums are read and written
-// once (they sit in L2), the order of the additions is fixed.
-__global__ void __launch_bounds__(256) decay_scan_kernel(float4* __restrict__ sums,
-                                                         const float4* first, float4* final_state,
+// (2) The sums of a head's segments -> the state at each one's entering side,
+// in place; the state behind the last one -> final_state.  One thread per 4
+// elements, segments in the walk's order: sums are read and written once (they
+// sit in L2), the order of the additions is fixed.
+//
+// The segments are the uniform ones of the fp32 kernels, or the pieces of the
+// tensor-core kernels with their packed sums (units of 4 columns, rows
+// adjacent).
+struct UniformSegments {
+  DecayPlan P;
+  static constexpr bool packed = false;
+  __device__ int count(int) const { return P.segs; }
+  __device__ int tokens_before(int, int i) const { return i * P.seg_len; }
+  __device__ int cap(int, int) const { return P.seg_len; }
+  __device__ i64 place(int bh, int i) const { return i64(bh) * P.segs + i; }
+};
+struct PieceSegments {
+  DecayParts P;
+  static constexpr bool packed = true;
+  // the part that holds chunk g: the last k with total k / parts <= g
+  __device__ int part(i64 g) const { return static_cast<int>(((g + 1) * P.parts - 1) / P.total); }
+  __device__ int first(int bh) const { return part(i64(bh) * P.chunks); }
+  __device__ int count(int bh) const { return part(i64(bh + 1) * P.chunks - 1) - first(bh) + 1; }
+  __device__ int tokens_before(int bh, int i) const {
+    return static_cast<int>(max(P.begin(first(bh) + i) - i64(bh) * P.chunks, i64(0))) * 128;
+  }
+  __device__ int cap(int bh, int i) const {
+    return static_cast<int>(min(P.begin(first(bh) + i + 1) - i64(bh) * P.chunks, i64(P.chunks))) * 128 -
+           tokens_before(bh, i);
+  }
+  __device__ i64 place(int bh, int i) const { return i64(first(bh)) + i + bh; }
+};
+
+constexpr int kScan = 14;  // segments' sums in flight per thread
+template <typename Segments>
+__global__ void __launch_bounds__(128) decay_scan_kernel(float4* __restrict__ sums, const float* first,
+                                                         bool turned, float4* final_state,
                                                          const float* __restrict__ log_decay,
-                                                         const int32_t* __restrict__ lens, DecayPlan P,
-                                                         int dd4, bool reverse) {
-  const int u = blockIdx.x * 256 + threadIdx.x;
+                                                         const int32_t* __restrict__ lens, Segments G,
+                                                         int d, bool reverse) {
+  const int dd4 = d * d / 4;
+  const int u = blockIdx.x * 128 + threadIdx.x;
   const int bh = blockIdx.y;
   if (u >= dd4) return;
-  const double l2 = decay_log2(log_decay[bh % P.H]);
-  const int len = sequence_tokens(P, lens, bh / P.H);
-  float4 s = first ? first[i64(bh) * dd4 + u] : make_float4(0.f, 0.f, 0.f, 0.f);
-  float4* row = sums + i64(bh) * P.segs * dd4 + u;
-  const float2 full = decay_power2(l2, P.seg_len);
-  for (int i0 = 0; i0 < P.segs; i0 += 8) {
-    float4 x[8];
+  const int r = G.packed ? u % d : u / (d / 4), c = G.packed ? u / d * 4 : u % (d / 4) * 4;
+  const double l2 = decay_log2(log_decay[bh % G.P.H]);
+  const int len = decay_tokens(lens, bh / G.P.H, G.P.N);
+  const int segs = G.count(bh);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (first) {
+    const float* f = first + i64(bh) * d * d;
+    s = turned ? make_float4(f[c * d + r], f[(c + 1) * d + r], f[(c + 2) * d + r], f[(c + 3) * d + r])
+               : *reinterpret_cast<const float4*>(f + r * d + c);
+  }
+  int n0 = -1;  // tokens that f stands for: most segments have the same
+  float2 f = make_float2(1.f, 0.f);
+  for (int i0 = 0; i0 < segs; i0 += kScan) {
+    float4 x[kScan];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int seg = reverse ? P.segs - 1 - (i0 + i) : i0 + i;
-      if (i0 + i < P.segs) x[i] = row[i64(seg) * dd4];
-    }
+    for (int i = 0; i < kScan; ++i)
+      if (i0 + i < segs) x[i] = sums[G.place(bh, reverse ? segs - 1 - (i0 + i) : i0 + i) * dd4 + u];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i0 + i < P.segs) {
-        const int seg = reverse ? P.segs - 1 - (i0 + i) : i0 + i;
-        row[i64(seg) * dd4] = s;
-        const int n = min(max(len - seg * P.seg_len, 0), P.seg_len);
-        const float2 f = n == P.seg_len ? full : decay_power2(l2, n);
+    for (int i = 0; i < kScan; ++i) {
+      if (i0 + i < segs) {
+        const int seg = reverse ? segs - 1 - (i0 + i) : i0 + i;
+        sums[G.place(bh, seg) * dd4 + u] = s;
+        const int n = min(max(len - G.tokens_before(bh, seg), 0), G.cap(bh, seg));
+        if (n != n0) {
+          f = decay_power2(l2, n);
+          n0 = n;
+        }
         s.x = fmaf(f.x, s.x, fmaf(f.y, s.x, x[i].x)); s.y = fmaf(f.x, s.y, fmaf(f.y, s.y, x[i].y));
         s.z = fmaf(f.x, s.z, fmaf(f.y, s.z, x[i].z)); s.w = fmaf(f.x, s.w, fmaf(f.y, s.w, x[i].w));
       }
     }
   }
-  if (final_state) final_state[i64(bh) * dd4 + u] = s;
+  if (final_state) final_state[i64(bh) * dd4 + r * (d / 4) + c / 4] = s;
 }
 
 // Few tokens: the state is read and written once, by CTAs that own 32 columns
@@ -408,10 +448,18 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
 cudaError_t launch_decay_scan(float* sums, const float* first, float* final_state,
                               const float* log_decay, const int32_t* lens, const DecayPlan& P,
                               bool reverse, const Geom& g, cudaStream_t s) {
-  const int dd4 = g.d * g.d / 4;
-  decay_scan_kernel<<<dim3((dd4 + 255) / 256, g.BH), 256, 0, s>>>(
-      reinterpret_cast<float4*>(sums), reinterpret_cast<const float4*>(first),
-      reinterpret_cast<float4*>(final_state), log_decay, lens, P, dd4, reverse);
+  decay_scan_kernel<<<dim3(g.d * g.d / 512, g.BH), 128, 0, s>>>(
+      reinterpret_cast<float4*>(sums), first, false, reinterpret_cast<float4*>(final_state), log_decay,
+      lens, UniformSegments{P}, g.d, reverse);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decay_scan_parts(float* sums, const float* first, bool turned, float* final_state,
+                                    const float* log_decay, const int32_t* lens, const DecayParts& P,
+                                    bool reverse, const Geom& g, cudaStream_t s) {
+  decay_scan_kernel<<<dim3(g.d * g.d / 512, g.BH), 128, 0, s>>>(
+      reinterpret_cast<float4*>(sums), first, turned, reinterpret_cast<float4*>(final_state), log_decay,
+      lens, PieceSegments{P}, g.d, reverse);
   return cudaGetLastError();
 }
 

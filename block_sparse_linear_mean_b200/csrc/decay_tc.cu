@@ -4,15 +4,20 @@
 // Chunks of 128 tokens.  Per chunk, with S the state at its entering side:
 //   X = a b^T                                    (K-major x K-major)
 //   P = X o D, D_ij = w_in decay^(i-j)           (registers, bf16 into TMEM)
-//   Z = a bf16(S),  O = P c                      (TMEM A for P)
-//   out_i = O_i + w_st decay^(i+1-e) Z_i         (registers, fp32)
-//   S <- decay^n S + (w b)^T c                   (accumulates in TMEM)
+//   O = diag(w_st decay^(i+1-e)) a S + P c       (a S is scaled in TMEM between
+//                                                 the two products)
+//   S <- decay^n S + (w b)^T c
 //
-// Roundings to bf16 beside the inputs' own: P, S as operand of Z, and w b:
-// one each per term of a bf16 result.  The state that is handed on (to the
-// next segment, to the caller) does not come from there: decay_sums_tc
-// splits w b into three bf16 parts (hi + lo + lo2, 24 bits together), so
-// its sums have fp32 accuracy.
+// Shared memory's bandwidth is what the products compete for (each reads both
+// operands again for every 16 tokens), so the weighted operand (w b)^T never
+// goes there: an identity product, T = b^T I, brings b^T into TMEM exactly,
+// with channels as lanes and tokens as columns; registers weight it and put
+// it back as bf16 parts, an A operand in TMEM.
+//
+// Roundings to bf16 beside the inputs' own: P, and S as operand, once per
+// term of a bf16 result.  w b is split into two parts (hi + lo, 16 bits) in
+// the output kernel and into three (24 bits) in the sums, whose states are
+// handed on and keep fp32 accuracy.
 #include <algorithm>
 
 #include "common.cuh"
@@ -24,7 +29,6 @@ namespace sla {
 namespace {
 
 constexpr int kC = 128;            // tokens per chunk
-constexpr int kThreads = 320;      // 8 worker warps, loader, issuer
 
 __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   const uint32_t a = smem_u32(p);
@@ -61,36 +65,102 @@ __device__ __forceinline__ void drain(bool ok) {
   }
 }
 
-// Token rows [t0 + 128 n, + nc) of a segment of n_tok real tokens at t0; the
-// walk goes over n from the entering side.
-struct Chunks {
-  int t0, tokens, count;
+// The piece of a head that a CTA works on, in steps of T rows walked from one
+// side or the other.
+template <int T>
+struct Piece {
+  int bh, index;       // head, place in the sums' workspace
+  int t0, cap;         // first token, tokens of the piece
+  int tokens, count;   // real ones, steps
   bool reverse;
   __device__ __forceinline__ int at(int n) const { return reverse ? count - 1 - n : n; }
-  __device__ __forceinline__ int row(int n) const { return t0 + at(n) * kC; }
-  __device__ __forceinline__ int size(int n) const { return min(kC, tokens - at(n) * kC); }
+  __device__ __forceinline__ int row(int n) const { return t0 + at(n) * T; }
+  __device__ __forceinline__ int size(int n) const { return min(T, tokens - at(n) * T); }
 };
+template <int T>
+__device__ __forceinline__ Piece<T> get_piece(const DecayParts& P, const int32_t* lens, int part, int bh,
+                                              bool reverse) {
+  const i64 head = i64(bh) * P.chunks;
+  const int c0 = static_cast<int>(max(P.begin(part), head) - head);
+  const int c1 = static_cast<int>(min(P.begin(part + 1), head + P.chunks) - head);
+  Piece<T> x;
+  x.bh = bh;
+  x.index = part + bh;
+  x.t0 = c0 * kC;
+  x.cap = min(c1 * kC, P.N) - x.t0;
+  x.tokens = min(max(decay_tokens(lens, bh / P.H, P.N) - x.t0, 0), x.cap);
+  x.count = (x.tokens + T - 1) / T;
+  x.reverse = reverse;
+  return x;
+}
 
-// [128][D] tile as D / 64 swizzled halves of 16 KB each.
+// A [rows][D] tile as D / 64 swizzled halves of `half` bytes each.
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int row, int bh,
-                                          uint32_t bar) {
+                                          uint32_t bar, uint32_t half) {
 #pragma unroll
-  for (int h = 0; h < D / 64; ++h) tma_load_3d(dst + h * 16384, map, h * 64, row, bh, bar);
+  for (int h = 0; h < D / 64; ++h) tma_load_3d(dst + h * half, map, h * 64, row, bh, bar);
 }
 
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// I16 for the identity product, [16][16] bf16 without swizzle: core matrices
+// of 8 rows x 16 bytes, the two on the diagonal I8, the others zero (the same
+// whichever of the two offsets runs along K).
+constexpr uint32_t kEyeBytes = 512;
+__device__ __forceinline__ void write_eye(uint8_t* p, int tid) {
+  if (tid < 128) {
+    const int core = tid >> 5, row = tid >> 2 & 7, pair = tid & 3;  // two elements per thread
+    uint32_t v = 0u;
+    if ((core == 0 || core == 3) && row >> 1 == pair) v = row & 1 ? 0x3F800000u : 0x00003F80u;
+    reinterpret_cast<uint32_t*>(p)[tid] = v;
+  }
+}
+__device__ __forceinline__ uint64_t eye_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(256 >> 4) << 32) | (1ull << 46);
+}
+
+// Clears rows [nc, T) of a [T][D] tile pair (b, c): nothing but zeros may
+// stand behind a weight of zero.
+template <int D, int T>
+__device__ __forceinline__ void clear_rows(uint8_t* b, uint8_t* c, int nc, int thread, int threads) {
+  for (int x = thread; x < (T - nc) * (D / 8); x += threads) {
+    const int r = nc + x / (D / 8), u = x % (D / 8);
+    const uint32_t off = (u >> 3) * (T * 128) + sw128(r, u & 7);
+    *reinterpret_cast<uint4*>(b + off) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(c + off) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Sixteen values of a row into a bf16 part; v keeps what the part leaves.
+__device__ __forceinline__ void take_part(float* v, uint32_t* part) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    part[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+    v[2 * x] -= lo_bf16(part[x]);
+    v[2 * x + 1] -= hi_bf16(part[x]);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Segment sums: sums[bh][seg] = w_sum sum_i decay^(n-1-i+e) b_i^T c_i.
 //
-// Weights count from the segment's far end, so the accumulator is never
-// scaled and the chunks' order is free: from the leaving side to the entering
-// one, so that what the output kernel reads first was read last and is still
-// in L2.  Eight warps turn a b tile into its three weighted parts (hi in
-// place), the issuer multiplies.  With d = 64 hi and lo are stacked to the 128
-// rows of one product and lo2 goes to an accumulator of its own.
+// Weights count from the piece's far end, so nothing is scaled on the way and
+// the order of the tokens is free: from the leaving side to the entering one,
+// so that what the output kernel reads first was read last and is still in
+// L2.  Steps of 64 tokens; two groups of eight warps take them in turn, one's
+// arithmetic under the other's products.
+//
+// The tensor core truncates as it accumulates: one chain over ten thousand
+// tokens loses 2^-17 of the sum.  So every four steps the accumulator (two of
+// them, in turn) is added to fp32 registers, and within a step the small parts
+// go first.
+constexpr int kThreads = 576;      // 16 worker warps, loader, issuer
+constexpr int kT = 64;             // tokens per step
+constexpr int kFlush = 4;          // steps per accumulation
+
 struct SumsRole {
   float w_sum;
   int e;
@@ -99,12 +169,15 @@ struct SumsRole {
 
 template <int D>
 struct SumsSmem {
-  static constexpr uint32_t tile = 128 * D * 2;
+  static constexpr uint32_t half = kT * 128;           // [64 tokens][64 channels]
+  static constexpr uint32_t tile = kT * D * 2;
   static constexpr uint32_t stage = 2 * tile;          // b, c
-  static constexpr uint32_t off_lo = 2 * stage;        // d = 128: lo, lo2; d = 64: lo2, hi, lo
-  static constexpr uint32_t parts = D == 128 ? 2 : 3;
-  static constexpr uint32_t off_bar = off_lo + parts * tile;
-  static constexpr uint32_t total = off_bar + 128 + 512 + 1024;
+  static constexpr int stages = 6;
+  static constexpr uint32_t off_eye = stages * stage;
+  static constexpr uint32_t off_bar = off_eye + kEyeBytes;
+  static constexpr uint32_t off_tab = off_bar + 256;
+  static constexpr uint32_t used = off_tab + 1024;
+  static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM
 };
 
 template <int D>
@@ -112,509 +185,673 @@ __global__ void __launch_bounds__(kThreads, 1)
     decay_sums_tc(const __grid_constant__ CUtensorMap mb0, const __grid_constant__ CUtensorMap mc0,
                   const __grid_constant__ CUtensorMap mb1, const __grid_constant__ CUtensorMap mc1,
                   const float* __restrict__ log_decay, const int32_t* __restrict__ lens,
-                  float* __restrict__ sums0, float* __restrict__ sums1, DecayPlan P, SumsRole R0,
+                  float* __restrict__ sums0, float* __restrict__ sums1, DecayParts P, SumsRole R0,
                   SumsRole R1, int32_t* status, int32_t* zero, long long limit, int withhold) {
   using L = SumsSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1k(smem_raw);
   const uint32_t sb = smem_u32(base);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::off_bar);
-  const uint32_t b_full = smem_u32(bars), b_empty = smem_u32(bars + 2), b_ready = smem_u32(bars + 4),
-                 b_done = smem_u32(bars + 5);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 6);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 7);
-  float* pw = reinterpret_cast<float*>(base + L::off_bar + 128);  // decay^k, k < 128
+  const uint32_t b_full = smem_u32(bars), b_empty = smem_u32(bars + 6);
+  const uint32_t b_t = smem_u32(bars + 12);      // [2] T in TMEM
+  const uint32_t b_ready = smem_u32(bars + 14);  // [2] parts in TMEM
+  const uint32_t b_acc = smem_u32(bars + 16);    // [2] an accumulation is complete
+  const uint32_t b_flush = smem_u32(bars + 18);  // [2] and has been read
+  const uint32_t b_clear = smem_u32(bars + 20);  // [2] rows behind the end cleared, by group
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 22);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 23);
+  float* pw = reinterpret_cast<float*>(base + L::off_tab);  // decay^k by place in a step, per head parity
   const int tid = threadIdx.x, warp = tid / 32;
-  const int seg = blockIdx.x, bh = blockIdx.y;
-  const bool second = blockIdx.z != 0;
+  const int part = blockIdx.x;
+  const bool second = blockIdx.y != 0;
   const SumsRole R = second ? R1 : R0;
   const CUtensorMap* mb = second ? &mb1 : &mb0;
   const CUtensorMap* mc = second ? &mc1 : &mc0;
-  if (zero && tid == 0 && seg == 0 && bh == 0 && !second) *zero = 0;
-  const double l2 = decay_log2(log_decay[bh % P.H]);
-  const int n = segment_tokens(P, lens, bh / P.H, seg);
-  const Chunks ch{seg * P.seg_len, n, (n + kC - 1) / kC, R.reverse == 0};  // against the direction
+  if (zero && tid == 0 && part == 0 && !second) *zero = 0;
+  const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
+  const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
+  const bool rev = R.reverse == 0;  // against the direction of the walk
   if (tid == 0) {
-    mbar_init(b_full, 1);
-    mbar_init(b_full + 8, 1);
-    mbar_init(b_empty, 1);
-    mbar_init(b_empty + 8, 1);
-    mbar_init(b_ready, 8);
-    mbar_init(b_done, 1);
+    for (int x = 0; x < 12; ++x) mbar_init(smem_u32(bars + x), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(b_t + 8 * x, 1);
+      mbar_init(b_ready + 8 * x, 8);
+      mbar_init(b_acc + 8 * x, 1);
+      mbar_init(b_flush + 8 * x, 16);
+      mbar_init(b_clear + 8 * x, 8);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < kC) pw[tid] = decay_power(l2, tid);
-  if (warp == 9) tmem_alloc(smem_u32(tslot), 128);
+  write_eye(base + L::off_eye, tid);
+  if (warp == 17) tmem_alloc(smem_u32(tslot), 512);
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // buffer q at 128 q: T at columns 0 .. 63, over 16 tokens' columns their hi
+  // (8) and lo parts (8); lo2 at 64 .. 95.  Accumulators at 256 and 384
   const uint32_t tmem = *tslot;
   const Waiter wait{status, abort_flag, limit};
+  const unsigned all = 0xffffffffu;
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp == 16) {
     if (tid % 32 == 0) {
-      for (int i = 0; ok && i < ch.count; ++i) {
-        const int s = i & 1;
-        if (i >= 2) ok = wait(b_empty + 8 * s, ((i >> 1) & 1) ^ 1);
-        if (!ok) break;
-        mbar_expect_tx(b_full + 8 * s, L::stage);
-        if (!(withhold && i == 0 && seg == 0 && bh == 0))
-          load_tile<D>(sb + s * L::stage, mb, ch.row(i), bh, b_full + 8 * s);
-        load_tile<D>(sb + s * L::stage + L::tile, mc, ch.row(i), bh, b_full + 8 * s);
+      int s = 0, ph = 1, j = 0;
+      for (int bh = bh0; ok && bh <= bh1; ++bh) {
+        const Piece<kT> pc = get_piece<kT>(P, lens, part, bh, rev);
+        for (int i = 0; i < pc.count; ++i, ++j) {
+          if (j >= L::stages && !(ok = wait(b_empty + 8 * s, ph))) break;
+          mbar_expect_tx(b_full + 8 * s, L::stage);
+          if (!(withhold && j == 0 && part == 0))
+            load_tile<D>(sb + s * L::stage, mb, pc.row(i), bh, b_full + 8 * s, L::half);
+          load_tile<D>(sb + s * L::stage + L::tile, mc, pc.row(i), bh, b_full + 8 * s, L::half);
+          if (++s == L::stages) { s = 0; ph ^= 1; }
+        }
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     if (tid % 32 == 0) {
-      constexpr uint32_t idesc = idesc_bf16(128, D, 1, 1);
-      for (int i = 0; ok && i < ch.count; ++i) {
-        const int s = i & 1;
-        ok = wait(b_full + 8 * s, (i >> 1) & 1) && wait(b_ready, i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t dc = sdesc(sb + s * L::stage + L::tile, 16384, 1024);
-        const uint64_t dh = sdesc(D == 128 ? sb + s * L::stage : sb + L::off_lo + L::tile, 16384, 1024);
-        const uint64_t d2 = sdesc(sb + L::off_lo, 16384, 1024);
-        const uint64_t d3 = sdesc(sb + L::off_lo + L::tile, 16384, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t c = sdesc_add(dc, kk * 2048);
-          const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
-          tc_mma(tmem, sdesc_add(dh, kk * 2048), c, idesc, acc);
-          if constexpr (D == 128) {
-            tc_mma(tmem, sdesc_add(d2, kk * 2048), c, idesc, 1u);
-            tc_mma(tmem, sdesc_add(d3, kk * 2048), c, idesc, 1u);
-          } else {
-            // rows 64 .. 127 take the tile behind lo2 (hi again); that half of
-            // this accumulator is not read
-            tc_mma(tmem + 64, sdesc_add(d2, kk * 2048), c, idesc, acc);
-          }
+      constexpr uint32_t id_t = idesc_bf16(128, 16, 1, 0), id_s = idesc_bf16(128, D, 0, 1);
+      const uint64_t eye = eye_desc(sb + L::off_eye);
+      int s = 0, ph = 0;          // stage of the next T
+      uint32_t clears = 0;        // bit q: parity of group q's next clearing
+      // T of step j (of `size` tokens) into buffer j & 1
+      auto issue_t = [&](int j, int size) -> bool {
+        if (!wait(b_full + 8 * s, ph)) return false;
+        if (size < kT) {
+          if (!wait(b_clear + 8 * (j & 1), clears >> (j & 1) & 1)) return false;
+          clears ^= 1u << (j & 1);
         }
-        tc_commit(b_done);
-        tc_commit(b_empty + 8 * s);
+        tc_fence_after();
+        // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
+        const uint64_t db = sdesc(sb + s * L::stage, L::half, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)
+          tc_mma(tmem + 128 * (j & 1) + 16 * kk, sdesc_add(db, kk * 2048), eye, id_t, 0u);
+        tc_commit(b_t + 8 * (j & 1));
+        if (++s == L::stages) { s = 0; ph ^= 1; }
+        return true;
+      };
+      int j = 0, m = 0, sm = 0;  // step, accumulation, stage of the products
+      Piece<kT> pc = get_piece<kT>(P, lens, part, bh0, rev);
+      int bh = bh0, i = 0;
+      while (bh <= bh1 && pc.count == 0) {
+        if (++bh <= bh1) pc = get_piece<kT>(P, lens, part, bh, rev);
+      }
+      bool more = bh <= bh1;
+      if (more) ok = issue_t(0, pc.size(0));
+      while (ok && more) {
+        const int place = i % kFlush;
+        const bool end = place == kFlush - 1 || i + 1 == pc.count;
+        // the step behind this one
+        if (++i == pc.count) {
+          i = 0;
+          do {
+            if (++bh <= bh1) pc = get_piece<kT>(P, lens, part, bh, rev);
+          } while (bh <= bh1 && pc.count == 0);
+          more = bh <= bh1;
+        }
+        // (a partial one is cleared by workers that may be waiting, at a piece's
+        // end, for the products of this step: those go first then)
+        const bool ahead = more && pc.size(i) == kT;
+        if (ahead && !(ok = issue_t(j + 1, kT))) break;
+        const int q = j & 1;
+        if (place == 0 && m >= 2 && !(ok = wait(b_flush + 8 * (m & 1), ((m >> 1) & 1) ^ 1))) break;
+        if (!(ok = wait(b_ready + 8 * q, (j >> 1) & 1))) break;
+        tc_fence_after();
+        const uint32_t td = tmem + 256 + 128 * (m & 1), tp = tmem + 128 * q, first = place != 0 ? 1u : 0u;
+        const uint64_t dc = sdesc(sb + sm * L::stage + L::tile, L::half, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)  // lo2
+          tc_mma_ts(td, tp + 64 + kk * 8, sdesc_add(dc, kk * 2048), id_s, kk > 0 ? 1u : first);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)  // lo
+          tc_mma_ts(td, tp + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_s, 1u);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)  // hi
+          tc_mma_ts(td, tp + kk * 16, sdesc_add(dc, kk * 2048), id_s, 1u);
+        tc_commit(b_empty + 8 * sm);
+        if (end) {
+          tc_commit(b_acc + 8 * (m & 1));
+          ++m;
+        }
+        if (++sm == L::stages) sm = 0;
+        if (more && !ahead && !(ok = issue_t(j + 1, pc.size(i)))) break;
+        ++j;
       }
     }
   } else {
-    for (int i = 0; ok && i < ch.count; ++i) {
-      const int s = i & 1, nc = ch.size(i);
-      // tokens left behind row r of the chunk, toward the leaving side
-      const int row0 = ch.at(i) * kC;
-      ok = __all_sync(0xffffffffu, wait(b_full + 8 * s, (i >> 1) & 1));
-      if (ok && i > 0) ok = __all_sync(0xffffffffu, wait(b_done, (i - 1) & 1));
-      if (!ok) break;
-      const int r = tid & 127;
-      // distance of the chunk's nearest real token from the leaving side
-      const int near = R.reverse ? row0 : n - row0 - nc;
-      const float far_w = R.w_sum * decay_power(l2, near + R.e);
-      const float w = r < nc ? far_w * pw[R.reverse ? r : nc - 1 - r] : 0.f;
-      uint8_t* bt = base + s * L::stage;
-      uint8_t* hi_t = D == 128 ? bt : base + L::off_lo + L::tile;
-      uint8_t* lo_t = base + L::off_lo + (D == 128 ? 0 : 2 * L::tile);
-      uint8_t* l2_t = base + L::off_lo + (D == 128 ? L::tile : 0);
-      constexpr int U = D / 16;  // 16-byte units per thread: half a row
-#pragma unroll 4
-      for (int x = 0; x < U; ++x) {
-        const int u = (tid >> 7) * U + x;
-        const uint32_t off = (u >> 3) * 16384 + sw128(r, u & 7);
-        uint4 q = *reinterpret_cast<const uint4*>(bt + off);
-        if (r >= nc) {
-          q = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(bt + L::tile + off) = q;  // c: nothing may stand behind a weight of 0
-        }
-        uint32_t in[4] = {q.x, q.y, q.z, q.w}, h[4], l[4], m[4];
+    const int quad = warp & 3, group = warp >> 3, h = warp >> 2 & 1;
+    const uint32_t lane = static_cast<uint32_t>(quad * 32) << 16;
+    const int row = tid & 127;
+    constexpr int CW = D / 4;      // columns of the sum that a thread keeps
+    const int col0 = (warp >> 2) * CW;
+    const bool mine = D == 128 || quad < 2;
+    float acc[CW];
+    int j = 0, m = 0, s = 0, ph = 0;
+    bool pending = false;          // an accumulation to be read
+    auto flush = [&]() -> bool {
+      if (!__all_sync(all, wait(b_acc + 8 * (m & 1), (m >> 1) & 1))) return false;
+      tc_fence_after();
+      const uint32_t td = tmem + 256 + 128 * (m & 1) + lane + col0;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float a = w * lo_bf16(in[y]), b = w * hi_bf16(in[y]);
-          h[y] = pack_bf16x2(a, b);
-          const float a1 = a - lo_bf16(h[y]), b1 = b - hi_bf16(h[y]);
-          l[y] = pack_bf16x2(a1, b1);
-          m[y] = pack_bf16x2(a1 - lo_bf16(l[y]), b1 - hi_bf16(l[y]));
-        }
-        *reinterpret_cast<uint4*>(hi_t + off) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo_t + off) = make_uint4(l[0], l[1], l[2], l[3]);
-        *reinterpret_cast<uint4*>(l2_t + off) = make_uint4(m[0], m[1], m[2], m[3]);
+      for (int c = 0; c < CW; c += 16) {
+        float v[16];
+        tmem_ld16(td + c, v);
+        tmem_wait_ld();
+        reg_fence<16>(v);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[c + x] += v[x];
       }
-      fence_async_smem();
+      tc_fence_before();
       __syncwarp();
-      if (tid % 32 == 0) mbar_arrive(b_ready);
+      if (tid % 32 == 0) mbar_arrive(b_flush + 8 * (m & 1));
+      ++m;
+      pending = false;
+      return true;
+    };
+    for (int bh = bh0; bh <= bh1; ++bh) {
+      const Piece<kT> pc = get_piece<kT>(P, lens, part, bh, rev);
+      const double l2 = decay_log2(log_decay[bh % P.H]);
+      // the group's own table of decay^(place in a full step); every warp
+      // comes here, also one whose wait gave up
+      float* tab = pw + 64 * group;
+      if (!(ok = bar_sync_and(1 + group, 256, ok))) break;
+      if ((tid & 255) < kT) tab[tid & 255] = decay_power(l2, R.reverse ? tid & 255 : kT - 1 - (tid & 255));
+      asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory");
+#pragma unroll
+      for (int x = 0; x < CW; ++x) acc[x] = 0.f;
+      for (int i = 0; ok && i < pc.count; ++i, ++j) {
+        if ((j & 1) == group) {
+          const int nc = pc.size(i), row0 = pc.at(i) * kT;
+          // distance of the step's near edge from the leaving side: the table
+          // counts whole steps, and a partial one ends early (forward)
+          const int near = R.reverse ? row0 : pc.tokens - row0 - kT;
+          const float far_w = R.w_sum * decay_power(l2, max(near, 0) + R.e);
+          const uint32_t tT = tmem + 128 * group + lane;
+          if (nc < kT) {
+            if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
+            uint8_t* bt = base + s * L::stage;
+            clear_rows<D, kT>(bt, bt + L::tile, nc, tid & 255, 256);
+            fence_async_smem();
+            __syncwarp();
+            if (tid % 32 == 0) mbar_arrive(b_clear + 8 * group);
+          }
+          if (!(ok = __all_sync(all, wait(b_t + 8 * group, (j >> 1) & 1)))) break;
+          tc_fence_after();
+          if (mine) {
+            float v[32];
+            tmem_ld32(tT + 32 * h, v);
+            tmem_wait_ld();
+            reg_fence<32>(v);
+            const float2 fw = make_float2(far_w, far_w);
+            if (near >= 0) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(tab + 32 * h + x);
+                const float2 a = mul2(make_float2(v[x], v[x + 1]), mul2(fw, make_float2(w.x, w.y)));
+                const float2 b = mul2(make_float2(v[x + 2], v[x + 3]), mul2(fw, make_float2(w.z, w.w)));
+                v[x] = a.x; v[x + 1] = a.y; v[x + 2] = b.x; v[x + 3] = b.y;
+              }
+            } else {  // forward, partial: token nc - 1 is the near edge
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] *= far_w * tab[min(32 * h + x + kT - nc, kT - 1)];
+            }
+            // the 16 columns read take hi and lo of their tokens
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+              uint32_t p[8];
+              const uint32_t t = tT + 32 * h + c;
+              take_part(v + c, p);
+              tmem_st8u(t, p);
+              take_part(v + c, p);
+              tmem_st8u(t + 8, p);
+              take_part(v + c, p);
+              tmem_st8u(tT + 64 + 16 * h + c / 2, p);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (tid % 32 == 0) mbar_arrive(b_ready + 8 * group);
+        }
+        if (pending && !(ok = flush())) break;
+        pending = i % kFlush == kFlush - 1 || i + 1 == pc.count;
+        if (++s == L::stages) { s = 0; ph ^= 1; }
+      }
+      if (ok && pending) ok = flush();
+      // units of 4 columns, rows adjacent (the packed layout of the workspace)
+      if (ok && row < D) {
+        float4* dst = reinterpret_cast<float4*>(second ? sums1 : sums0) + i64(pc.index) * (D * D / 4);
+#pragma unroll
+        for (int x = 0; x < CW; x += 4)
+          dst[(col0 + x) / 4 * D + row] = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
+      }
     }
-    if (ok && ch.count > 0) ok = __all_sync(0xffffffffu, wait(b_done, (ch.count - 1) & 1));
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   ok = __syncthreads_and(ok && !*abort_flag);
-  // the accumulator, row = channel of b, to global memory
-  float* dst = (second ? sums1 : sums0) + (i64(bh) * P.segs + seg) * D * D;
-  if (ok && ch.count > 0) {
-    tc_fence_after();
-    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    if constexpr (D == 128) {
-      if (warp < 8) {
-        const int row = tid & 127, c0 = (warp >> 2) * 64;
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float v[32];
-          tmem_ld32(tmem + lane + c0 + c, v);
-          tmem_wait_ld();
-          reg_fence<32>(v);
-#pragma unroll
-          for (int x = 0; x < 32; x += 4)
-            *reinterpret_cast<float4*>(dst + row * D + c0 + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
-        }
-      }
-    } else {
-      // rows 64 .. 127 hold the lo parts: through shared memory to the warps
-      // of rows 0 .. 63 (stage 0 is free)
-      float* xch = reinterpret_cast<float*>(base);
-      if (warp == 2 || warp == 3) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float v[32];
-          tmem_ld32(tmem + lane + c, v);
-          tmem_wait_ld();
-          reg_fence<32>(v);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) xch[(c + x) * 64 + (tid & 63)] = v[x];
-        }
-      }
-      __syncthreads();
-      if (warp < 2) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float v[32], m[32];
-          tmem_ld32(tmem + lane + c, v);
-          tmem_ld32(tmem + lane + 64 + c, m);
-          tmem_wait_ld();
-          reg_fence<32>(v);
-          reg_fence<32>(m);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] += xch[(c + x) * 64 + tid] + m[x];
-#pragma unroll
-          for (int x = 0; x < 32; x += 4)
-            *reinterpret_cast<float4*>(dst + tid * D + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
-        }
-      }
-    }
-  } else if (ok) {
-    for (int u = tid; u < D * D; u += kThreads) dst[u] = 0.f;  // no token
-  }
   drain(ok);
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Outputs of a segment, chunk by chunk.  Warps 0-3 (row = thread) turn X into
-// P and write the results; warps 4-7 take the state from TMEM to its bf16
-// copy and weight the b tile in place; warp 8 loads, warp 9 issues.
+// Outputs of a segment, chunk by chunk.  Groups of warps, each thread a row:
+// four warps turn X into P; eight (two threads a row) weight T into its parts
+// and carry the state, fp32 in registers, bf16 in shared memory as operand;
+// four scale Z and bring out the results, through the a tile and a TMA store.
+// Then a loader and an issuer warp.
+//
+// Where the state of a piece's entering side stands: element (row, col) at
+// base + (row / 4) * r4 + (row % 4) * r1 + (col / 4) * c4 + (col % 4) * c1.
+struct StateView {
+  const float* base;
+  i64 stride;          // of the piece's place, or of the head
+  int by_piece;
+  int r4, r1, c4, c1;
+};
+
 template <int D>
 struct OutSmem {
   static constexpr uint32_t tile = 128 * D * 2;
   static constexpr uint32_t stage = 3 * tile;              // a, b, c
   static constexpr uint32_t off_s = 2 * stage;             // bf16 state, [d][d]
   static constexpr uint32_t s_bytes = D * D * 2;
-  static constexpr uint32_t off_bar = off_s + s_bytes;
-  static constexpr uint32_t off_tab = off_bar + 128;       // decay^k, k <= 128
-  static constexpr uint32_t total = off_tab + 130 * 4 + 1024;
+  static constexpr uint32_t off_eye = off_s + s_bytes;
+  static constexpr uint32_t off_bar = off_eye + kEyeBytes;
+  static constexpr uint32_t off_wt = off_bar + 160;        // the tokens' weights in a chunk
+  static constexpr uint32_t off_tab = off_wt + 512;        // decay^k, k <= 128
+  static constexpr uint32_t used = off_tab + 132 * 4 + 1024;
+  // one CTA per SM: it takes all of tensor memory
+  static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;
 };
 
 template <int D, bool REV>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_out_tc(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                 const __grid_constant__ CUtensorMap mc, const float* __restrict__ log_decay,
-                 const int32_t* __restrict__ lens, const float* __restrict__ starts, i64 start_stride,
-                 __nv_bfloat16* __restrict__ out, DecayPlan P, DecayRole R, int32_t* status,
-                 int32_t* zero, long long limit, int withhold) {
+                 const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap mo,
+                 const float* __restrict__ log_decay, const int32_t* __restrict__ lens,
+                 StateView start, __nv_bfloat16* __restrict__ out, DecayParts P, DecayRole R,
+                 int32_t* status, int32_t* zero, long long limit, int withhold) {
   using L = OutSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1k(smem_raw);
   const uint32_t sb = smem_u32(base);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::off_bar);
-  const uint32_t b_full = smem_u32(bars), b_empty = smem_u32(bars + 2);
-  const uint32_t b_x = smem_u32(bars + 4);    // X in TMEM
-  const uint32_t b_p = smem_u32(bars + 5);    // P in TMEM
-  const uint32_t b_o = smem_u32(bars + 6);    // O and Z in TMEM
-  const uint32_t b_free = smem_u32(bars + 7); // O and Z read
-  const uint32_t b_s = smem_u32(bars + 8);    // state updated
-  const uint32_t b_sr = smem_u32(bars + 9);   // bf16 state written, accumulator scaled
-  const uint32_t b_h = smem_u32(bars + 10);   // b weighted
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 11);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 12);
+  const uint32_t b_full = smem_u32(bars);
+  const uint32_t b_ea = smem_u32(bars + 2);    // a tile's results stored
+  const uint32_t b_ebc = smem_u32(bars + 4);   // b and c read
+  const uint32_t b_x = smem_u32(bars + 6);     // X in TMEM
+  const uint32_t b_t = smem_u32(bars + 7);     // T in TMEM
+  const uint32_t b_z = smem_u32(bars + 8);     // Z in TMEM (the bf16 state read)
+  const uint32_t b_u = smem_u32(bars + 9);     // (w b)^T c in TMEM
+  const uint32_t b_o = smem_u32(bars + 10);    // O in TMEM
+  const uint32_t b_p = smem_u32(bars + 11);    // P in TMEM
+  const uint32_t b_zs = smem_u32(bars + 12);   // Z scaled
+  const uint32_t b_free = smem_u32(bars + 13); // O read
+  const uint32_t b_w = smem_u32(bars + 14);    // parts in TMEM
+  const uint32_t b_sr = smem_u32(bars + 15);   // bf16 state written
+  const uint32_t b_clear = smem_u32(bars + 16);  // rows behind the end cleared
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 17);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 18);
   float* pw = reinterpret_cast<float*>(base + L::off_tab);
+  float* wt = reinterpret_cast<float*>(base + L::off_wt);
   const int tid = threadIdx.x, warp = tid / 32, quad = warp & 3;
-  const int seg = blockIdx.x, bh = blockIdx.y;
-  if (zero && tid == 0 && seg == 0 && bh == 0) *zero = 0;
-  const double l2 = decay_log2(log_decay[bh % P.H]);
-  const int n = segment_tokens(P, lens, bh / P.H, seg);
-  const Chunks ch{seg * P.seg_len, n, (n + kC - 1) / kC, REV};
+  const int part = blockIdx.x;
+  if (zero && tid == 0 && part == 0) *zero = 0;
+  const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
+  const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
   if (tid == 0) {
-    mbar_init(b_full, 1);
-    mbar_init(b_full + 8, 1);
-    mbar_init(b_empty, 1);
-    mbar_init(b_empty + 8, 1);
-    mbar_init(b_x, 1);
+    for (int x = 0; x < 11; ++x) mbar_init(smem_u32(bars + x), 1);
     mbar_init(b_p, 4);
-    mbar_init(b_o, 1);
+    mbar_init(b_zs, 4);
     mbar_init(b_free, 4);
-    mbar_init(b_s, 1);
-    mbar_init(b_sr, 4);
-    mbar_init(b_h, 4);
+    mbar_init(b_w, 8);
+    mbar_init(b_sr, 8);
+    mbar_init(b_clear, 4);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid <= kC) pw[tid] = decay_power(l2, tid);
-  if (warp == 9) tmem_alloc(smem_u32(tslot), 512);
+  write_eye(base + L::off_eye, tid);
+  if (warp == 17) tmem_alloc(smem_u32(tslot), 512);
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tX = *tslot, tO = tX + 128, tZ = tO + D, tS = tZ + D;  // P over X
+  // X under P; Z under O; T, over 16 tokens' columns their hi (8) and lo (8)
+  const uint32_t tX = *tslot, tO = tX + 128, tU = tX + 256, tT = tX + 384;
   const Waiter wait{status, abort_flag, limit};
   const unsigned all = 0xffffffffu;
+  const uint32_t lane = static_cast<uint32_t>(quad * 32) << 16;
+  const int r = tid & 127;
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp == 16) {
     if (tid % 32 == 0) {
-      for (int i = 0; ok && i < ch.count; ++i) {
-        const int s = i & 1;
-        if (i >= 2) ok = wait(b_empty + 8 * s, ((i >> 1) & 1) ^ 1);
-        if (!ok) break;
-        const uint32_t st = sb + s * L::stage, bar = b_full + 8 * s;
-        mbar_expect_tx(bar, L::stage);
-        if (!(withhold && i == 0 && seg == 0 && bh == 0)) load_tile<D>(st, &ma, ch.row(i), bh, bar);
-        load_tile<D>(st + L::tile, &mb, ch.row(i), bh, bar);
-        load_tile<D>(st + 2 * L::tile, &mc, ch.row(i), bh, bar);
+      int j = 0;
+      for (int bh = bh0; ok && bh <= bh1; ++bh) {
+        const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+        for (int i = 0; i < pc.count; ++i, ++j) {
+          const int s = j & 1;
+          const uint32_t st = sb + s * L::stage, bar = b_full + 8 * s, ph = ((j >> 1) & 1) ^ 1;
+          if (j >= 2 && !(ok = wait(b_ebc + 8 * s, ph))) break;
+          mbar_expect_tx(bar, L::stage);
+          load_tile<D>(st + L::tile, &mb, pc.row(i), bh, bar, 16384);
+          load_tile<D>(st + 2 * L::tile, &mc, pc.row(i), bh, bar, 16384);
+          if (j >= 2 && !(ok = wait(b_ea + 8 * s, ph))) break;
+          if (!(withhold && j == 0 && part == 0)) load_tile<D>(st, &ma, pc.row(i), bh, bar, 16384);
+        }
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     if (tid % 32 == 0) {
       constexpr uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1),
-                         id_s = idesc_bf16(128, D, 1, 1);
-      const uint64_t ds = sdesc(sb + L::off_s, D * 128, 1024);
-      for (int i = 0; i < ch.count; ++i) {
-        const int s = i & 1;
-        const uint32_t st = sb + s * L::stage;
-        const uint64_t da = sdesc(st, 16, 1024), db = sdesc(st + L::tile, 16, 1024);
-        const uint64_t dbt = sdesc(st + L::tile, 16384, 1024), dc = sdesc(st + 2 * L::tile, 16384, 1024);
-        if (!(ok = wait(b_full + 8 * s, (i >> 1) & 1))) break;
-        tc_fence_after();
+                         id_t = idesc_bf16(128, 16, 1, 0);
+      const uint64_t ds = sdesc(sb + L::off_s, D * 128, 1024), eye = eye_desc(sb + L::off_eye);
+      int j = 0, ju = 0, clears = 0;  // chunk; chunk that moves the state; partial chunk
+      for (int bh = bh0; ok && bh <= bh1; ++bh) {
+        const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+        for (int i = 0; i < pc.count; ++i, ++j) {
+          const int s = j & 1;
+          const bool last = i + 1 == pc.count;
+          const uint32_t st = sb + s * L::stage;
+          const uint64_t da = sdesc(st, 16, 1024), db = sdesc(st + L::tile, 16, 1024),
+                         dbt = sdesc(st + L::tile, 16384, 1024), dc = sdesc(st + 2 * L::tile, 16384, 1024);
+          if (!(ok = wait(b_full + 8 * s, (j >> 1) & 1))) break;
+          if (pc.size(i) < kC && !(ok = wait(b_clear, clears++ & 1))) break;
+          tc_fence_after();
+          // X = a b^T, over the P that the products before have read
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          tc_mma(tX, sdesc_add(da, off), sdesc_add(db, off), id_x, kk > 0);
-        }
-        tc_commit(b_x);
-        if (!(ok = wait(b_sr, i & 1))) break;
-        if (i > 0 && !(ok = wait(b_free, (i - 1) & 1))) break;
-        tc_fence_after();
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            tc_mma(tX, sdesc_add(da, off), sdesc_add(db, off), id_x, kk > 0);
+          }
+          tc_commit(b_x);
+          if (!last) {  // (behind a piece's last chunk nobody reads the state)
+            // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma(tZ, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_add(ds, kk * 2048), id_o, kk > 0);
-        if (!(ok = wait(b_h, i & 1))) break;
-        tc_fence_after();
-        if (i + 1 < ch.count) {  // (behind the last chunk nobody reads the state)
+            for (int kk = 0; kk < 8; ++kk) tc_mma(tT + 16 * kk, sdesc_add(dbt, kk * 2048), eye, id_t, 0u);
+            tc_commit(b_t);
+          }
+          // Z = a S
+          if (!(ok = wait(b_sr, j & 1))) break;
+          if (j > 0 && !(ok = wait(b_free, (j - 1) & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma(tO, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_add(ds, kk * 2048), id_o, kk > 0);
+          tc_commit(b_z);
+          // U = (w b)^T c
+          if (!last) {
+            if (!(ok = wait(b_w, ju & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ts(tU, tT + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_o, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ts(tU, tT + kk * 16, sdesc_add(dc, kk * 2048), id_o, 1u);
+            tc_commit(b_u);
+            ++ju;
+          }
+          // O = scaled Z + P c
+          if (!(ok = wait(b_p, j & 1) && wait(b_zs, j & 1))) break;
+          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc_mma(tS, sdesc_add(dbt, kk * 2048), sdesc_add(dc, kk * 2048), id_s, 1u);
-          tc_commit(b_s);
+            tc_mma_ts(tO, tX + kk * 8, sdesc_add(dc, kk * 2048), id_o, 1u);
+          tc_commit(b_o);
+          tc_commit(b_ebc + 8 * s);
         }
-        if (!(ok = wait(b_p, i & 1))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc_mma_ts(tO, tX + kk * 8, sdesc_add(dc, kk * 2048), id_o, kk > 0);
-        tc_commit(b_o);
-        tc_commit(b_empty + 8 * s);
       }
     }
   } else if (warp < 4) {
-    // ------------------------------------------------ P and the results
-    const int r = tid;
-    const uint32_t lane = static_cast<uint32_t>(quad * 32) << 16;
-    for (int i = 0; ok && i < ch.count; ++i) {
-      const int nc = ch.size(i);
-      if (!(ok = __all_sync(all, wait(b_x, i & 1)))) break;
-      tc_fence_after();
+    // ------------------------------------------------ P
+    int j = 0;
+    for (int bh = bh0; bh <= bh1; ++bh) {
+      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+      // (every warp comes here, also one whose wait gave up)
+      if (!(ok = bar_sync_and(1, 128, ok))) break;
+      pw[r] = R.w_in * decay_power(decay_log2(log_decay[bh % P.H]), r);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      for (int i = 0; ok && i < pc.count; ++i, ++j) {
+        const int nc = pc.size(i);
+        if (!(ok = __all_sync(all, wait(b_x, j & 1)))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
-        uint32_t pk[16];
-        // a block of 32 columns before (behind) all of the warp's rows is full,
-        // one behind (before) them empty, the one on the diagonal mixed
-        const bool empty = REV ? cb < quad : cb > quad;
-        if (empty) {
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t pk[16];
+          // a block of 32 columns before (behind) all of the warp's rows is
+          // full, one behind (before) them empty, the one on the diagonal mixed
+          const bool empty = REV ? cb < quad : cb > quad;
+          if (empty) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) pk[x] = 0u;
-        } else {
-          float v[32];
-          tmem_ld32(tX + lane + cb * 32, v);
-          tmem_wait_ld();
-          reg_fence<32>(v);
-          if (cb != quad && (!REV || nc == kC)) {
-            // decay^(i-j) = decay^(distance to the block's near end) times
-            // decay^(place within the block): no exponent is negative
-            const float f = R.w_in * pw[REV ? cb * 32 - r : r - cb * 32 - 31];
-            const float2 ff = make_float2(f, f);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float2 u = REV ? make_float2(pw[2 * x], pw[2 * x + 1])
-                                   : make_float2(pw[31 - 2 * x], pw[30 - 2 * x]);
-              const float2 y = mul2(make_float2(v[2 * x], v[2 * x + 1]), mul2(u, ff));
-              pk[x] = pack_bf16x2(y.x, y.y);
-            }
+            for (int x = 0; x < 16; ++x) pk[x] = 0u;
           } else {
+            float v[32];
+            tmem_ld32(tX + lane + cb * 32, v);
+            tmem_wait_ld();
+            reg_fence<32>(v);
+            const bool mixed = cb == quad || (REV && nc < kC);
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-              const int j = cb * 32 + x, gap = REV ? j - r : r - j;
-              const bool in = gap >= 0 && (!REV || j < nc);
-              v[x] = in ? v[x] * (R.w_in * pw[in ? gap : 0]) : 0.f;
+              const int jj = cb * 32 + x, gap = REV ? jj - r : r - jj;
+              const bool in = !mixed || (gap >= 0 && (!REV || jj < nc));
+              v[x] = in ? v[x] * pw[in ? gap : 0] : 0.f;
             }
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
           }
+          tmem_st16u(tX + lane + cb * 16, pk);
         }
-        tmem_st16u(tX + lane + cb * 16, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (tid % 32 == 0) mbar_arrive(b_p);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (tid % 32 == 0) mbar_arrive(b_p);
-      if (!(ok = __all_sync(all, wait(b_o, i & 1)))) break;
-      tc_fence_after();
-      const int row = ch.row(i) + r;
-      const int gap = REV ? nc - 1 - r : r;
-      const bool real = r < nc;
-      const float f = real ? R.w_st * pw[gap + 1 - R.e] : 0.f;
-      __nv_bfloat16* dst = out + (i64(bh) * P.N + row) * D;
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------ weights and state
+    const int h = (warp - 4) >> 2;       // half of the tokens (T), of the state's columns
+    constexpr int CW = D / 2;
+    const int col0 = h * CW;
+    const bool mine = D == 128 || quad < 2;  // (d = 64: rows 64 .. 127 are not used)
+    float S[CW];
+    int j = 0, ju = 0;
+    for (int bh = bh0; bh <= bh1; ++bh) {
+      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+      const double l2 = decay_log2(log_decay[bh % P.H]);
+      if (!(ok = bar_sync_and(2, 256, ok))) break;
+      const int k = tid - 128;
+      if (k < kC) wt[k] = R.w_sum * decay_power(l2, (REV ? k : kC - 1 - k) + R.e);
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (mine && start.base && pc.count > 0) {
+        const float* p = start.base + start.stride * (start.by_piece ? pc.index : bh) + (r >> 2) * start.r4 + (r & 3) * start.r1;
+        if (start.c1 == 1) {
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        float o[32], z[32];
-        tmem_ld32(tO + lane + c, o);
-        tmem_ld32(tZ + lane + c, z);
-        tmem_wait_ld();
-        reg_fence<32>(o);
-        reg_fence<32>(z);
-        if (c + 32 == D) {
+          for (int x = 0; x < CW; x += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(p + ((col0 + x) >> 2) * start.c4);
+            S[x] = f4.x; S[x + 1] = f4.y; S[x + 2] = f4.z; S[x + 3] = f4.w;
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < CW; ++x) S[x] = p[((col0 + x) >> 2) * start.c4 + (x & 3) * start.c1];
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < CW; ++x) S[x] = 0.f;
+      }
+      for (int i = 0; ok && i < pc.count; ++i, ++j) {
+        // the Z of the chunk before has read the last bf16 state
+        if (j > 0 && !(ok = __all_sync(all, wait(b_z, (j - 1) & 1)))) break;
+        if (mine) {
+#pragma unroll
+          for (int x = 0; x < CW; x += 8) {
+            const int u = (col0 + x) >> 3;
+            *reinterpret_cast<uint4*>(base + L::off_s + (u >> 3) * (D * 128) + sw128(r, u & 7)) =
+                make_uint4(pack_bf16x2(S[x], S[x + 1]), pack_bf16x2(S[x + 2], S[x + 3]),
+                           pack_bf16x2(S[x + 4], S[x + 5]), pack_bf16x2(S[x + 6], S[x + 7]));
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (tid % 32 == 0) mbar_arrive(b_sr);
+        if (i + 1 == pc.count) continue;
+        if (!(ok = __all_sync(all, wait(b_t, ju & 1)))) break;
+        tc_fence_after();
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            float v[16];
+            uint32_t p[8];
+            const uint32_t t = tT + lane + 64 * h + c;
+            tmem_ld16(t, v);
+            tmem_wait_ld();
+            reg_fence<16>(v);
+#pragma unroll
+            for (int x = 0; x < 16; x += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(wt + 64 * h + c + x);
+              v[x] *= w.x; v[x + 1] *= w.y; v[x + 2] *= w.z; v[x + 3] *= w.w;
+            }
+            // the 16 columns read take hi and lo of their tokens
+            take_part(v, p);
+            tmem_st8u(t, p);
+            take_part(v, p);
+            tmem_st8u(t + 8, p);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (tid % 32 == 0) mbar_arrive(b_w);
+        const float fs = decay_power(l2, pc.size(i));
+        if (!(ok = __all_sync(all, wait(b_u, ju & 1)))) break;
+        tc_fence_after();
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < CW; c += 16) {
+            float v[16];
+            tmem_ld16(tU + lane + col0 + c, v);
+            tmem_wait_ld();
+            reg_fence<16>(v);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) S[c + x] = fmaf(fs, S[c + x], v[x]);
+          }
+        }
+        tc_fence_before();
+        ++ju;
+      }
+    }
+  } else {
+    // ------------------------------------------------ results
+    int j = 0;
+    for (int bh = bh0; bh <= bh1; ++bh) {
+      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+      const double l2 = decay_log2(log_decay[bh % P.H]);
+      const float full = R.w_st * decay_power(l2, (REV ? kC - 1 - r : r) + 1 - R.e);
+      for (int i = 0; i < pc.count; ++i, ++j) {
+        const int s = j & 1, nc = pc.size(i);
+        const bool real = r < nc;
+        uint8_t* at = base + s * L::stage;
+        float f = full;
+        if (nc < kC) {
+          if (REV) f = real ? R.w_st * decay_power(l2, nc - r - R.e) : 0.f;
+          if (ok && (ok = __all_sync(all, wait(b_full + 8 * s, (j >> 1) & 1)))) {
+            clear_rows<D, kC>(at + L::tile, at + 2 * L::tile, nc, r, 128);
+            fence_async_smem();
+            __syncwarp();
+            if (tid % 32 == 0) mbar_arrive(b_clear);
+          }
+        }
+        if (ok && (ok = __all_sync(all, wait(b_z, j & 1)))) {
+          tc_fence_after();
+          const float2 ff = make_float2(f, f);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float z[32];
+            tmem_ld32(tO + lane + c, z);
+            tmem_wait_ld();
+            reg_fence<32>(z);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const float2 y = mul2(ff, make_float2(z[x], z[x + 1]));
+              z[x] = y.x;
+              z[x + 1] = y.y;
+            }
+            tmem_st32(tO + lane + c, z);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (tid % 32 == 0) mbar_arrive(b_zs);
+        }
+        if (ok && (ok = __all_sync(all, wait(b_o, j & 1)))) {
+          tc_fence_after();
+          uint32_t w[D / 2];
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tO + lane + c, o);
+            tmem_wait_ld();
+            reg_fence<32>(o);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) w[c / 2 + x] = real ? pack_bf16x2(o[2 * x], o[2 * x + 1]) : 0u;
+          }
+          // the next Z may come over O
           tc_fence_before();
           __syncwarp();
           if (tid % 32 == 0) mbar_arrive(b_free);
-        }
-        if (row < P.N) {
+          // all products that read this a tile are complete
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (real)
-              w = make_uint4(pack_bf16x2(fmaf(f, z[x], o[x]), fmaf(f, z[x + 1], o[x + 1])),
-                             pack_bf16x2(fmaf(f, z[x + 2], o[x + 2]), fmaf(f, z[x + 3], o[x + 3])),
-                             pack_bf16x2(fmaf(f, z[x + 4], o[x + 4]), fmaf(f, z[x + 5], o[x + 5])),
-                             pack_bf16x2(fmaf(f, z[x + 6], o[x + 6]), fmaf(f, z[x + 7], o[x + 7])));
-            *reinterpret_cast<uint4*>(dst + c + x) = w;
-          }
+          for (int u = 0; u < D / 8; ++u)
+            *reinterpret_cast<uint4*>(at + (u >> 3) * 16384 + sw128(r, u & 7)) =
+                make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+          fence_async_smem();
         }
+        // (every warp comes here, also one whose wait gave up)
+        if (!(ok = bar_sync_and(3, 128, ok))) break;
+        if (r == 0) {
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_store_3d(&mo, sb + s * L::stage + h * 16384, h * 64, pc.row(i), bh);
+          tma_store_commit();
+          tma_store_wait_read();
+          mbar_arrive(b_ea + 8 * s);
+        }
+      }
+      if (!ok) break;
+      // whole chunks behind the sequence's end
+      for (int t = pc.count * kC + r; t < pc.cap; t += kC) {
+        uint4* dst = reinterpret_cast<uint4*>(out + (i64(bh) * P.N + pc.t0 + t) * D);
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) dst[x] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    // whole chunks behind the sequence's end
-    const int seg_end = min(P.seg_len, P.N - ch.t0);
-    for (int t = ch.count * kC + r; t < seg_end; t += kC) {
-      uint4* dst = reinterpret_cast<uint4*>(out + (i64(bh) * P.N + ch.t0 + t) * D);
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x) dst[x] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  } else {
-    // ------------------------------------------------ state and weights
-    const int r = tid - 128;
-    const uint32_t lane = static_cast<uint32_t>(quad * 32) << 16;
-    const float* src = starts ? starts + i64(bh) * start_stride + i64(seg) * D * D : nullptr;
-    for (int i = 0; ok && i < ch.count; ++i) {
-      const int s = i & 1, nc = ch.size(i);
-      const float fs = pw[nc];
-      if (i > 0) {
-        if (!(ok = __all_sync(all, wait(b_s, (i - 1) & 1)))) break;
-        tc_fence_after();
-      }
-      if (r < D) {  // (d = 64: the accumulator's lower rows are not used)
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float v[32];
-          if (i > 0) {
-            tmem_ld32(tS + lane + c, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
-          } else if (!src) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = 0.f;
-          } else if (R.transposed) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = __ldg(src + (c + x) * D + r);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 f4 = __ldg(reinterpret_cast<const float4*>(src + r * D + c + x));
-              v[x] = f4.x; v[x + 1] = f4.y; v[x + 2] = f4.z; v[x + 3] = f4.w;
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            const int u = (c + x) >> 3;
-            *reinterpret_cast<uint4*>(base + L::off_s + (u >> 3) * (D * 128) + sw128(r, u & 7)) =
-                make_uint4(pack_bf16x2(v[x], v[x + 1]), pack_bf16x2(v[x + 2], v[x + 3]),
-                           pack_bf16x2(v[x + 4], v[x + 5]), pack_bf16x2(v[x + 6], v[x + 7]));
-          }
-#pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] *= fs;
-          tmem_st32(tS + lane + c, v);
-        }
-        tmem_wait_st();
-      }
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (tid % 32 == 0) mbar_arrive(b_sr);
-      // b <- w b in place, X = a b^T having been formed
-      if (!(ok = __all_sync(all, wait(b_full + 8 * s, (i >> 1) & 1) && wait(b_x, i & 1)))) break;
-      const float w = r < nc ? R.w_sum * pw[(REV ? r : nc - 1 - r) + R.e] : 0.f;
-      uint8_t* bt = base + s * L::stage + L::tile;
-      constexpr int U = D / 8;
-#pragma unroll 8
-      for (int u = 0; u < U; ++u) {
-        const uint32_t off = (u >> 3) * 16384 + sw128(r, u & 7);
-        uint4* p = reinterpret_cast<uint4*>(bt + off);
-        uint4 q = *p;
-        if (r >= nc) {
-          q = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(bt + L::tile + off) = q;  // c: nothing may stand behind a weight of 0
-        } else {
-          uint32_t* y = reinterpret_cast<uint32_t*>(&q);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) y[x] = pack_bf16x2(w * lo_bf16(y[x]), w * hi_bf16(y[x]));
-        }
-        *p = q;
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (tid % 32 == 0) mbar_arrive(b_h);
-    }
+    if (r == 0) tma_store_wait_all();
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   ok = __syncthreads_and(ok && !*abort_flag);
   drain(ok);
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tX, 512);
   }
 }
 
-bool token_map(CUtensorMap* m, const void* ptr, const Geom& g) {
+bool token_map(CUtensorMap* m, const void* ptr, const Geom& g, uint32_t rows) {
   const uint64_t dims[3] = {static_cast<uint64_t>(g.d), static_cast<uint64_t>(g.N),
                             static_cast<uint64_t>(g.BH)};
   const uint64_t strides[2] = {static_cast<uint64_t>(g.d) * 2, static_cast<uint64_t>(g.N) * g.d * 2};
-  const uint32_t box[3] = {64, kC, 1};
+  const uint32_t box[3] = {64, rows, 1};
   return encode_bf16_map(m, ptr, 3, dims, strides, box);
 }
 
@@ -625,48 +862,62 @@ cudaError_t set_smem(K kern, uint32_t bytes) {
 
 }  // namespace
 
-int decay_tc_chunk() { return kC; }
-
 bool decay_tc_supported(const Geom& g) {
   return g.dtype == SLA_BF16 && !(g.flags & SLA_FLAG_SIMT);
 }
 
+DecayParts decay_parts(const Geom& g) {
+  DecayParts P;
+  P.N = g.N;
+  P.H = g.H;
+  P.chunks = (g.N + kC - 1) / kC;
+  P.total = i64(P.chunks) * g.BH;
+  P.parts = static_cast<int>(std::min<i64>(P.total, 148));
+  return P;
+}
+
 cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* log_decay,
-                                 const int32_t* lens, const DecayPlan& P, const Geom& g,
+                                 const int32_t* lens, const DecayParts& P, const Geom& g,
                                  int32_t* status, int32_t* zero, cudaStream_t s) {
   CUtensorMap m[4];
   SumsRole r[2];
   for (int i = 0; i < 2; ++i) {
     const DecaySums& j = jobs[i < count ? i : 0];
-    if (!token_map(&m[2 * i], j.b, g) || !token_map(&m[2 * i + 1], j.c, g)) return cudaErrorInvalidValue;
+    if (!token_map(&m[2 * i], j.b, g, kT) || !token_map(&m[2 * i + 1], j.c, g, kT)) return cudaErrorInvalidValue;
     r[i] = SumsRole{j.w_sum, j.e, j.reverse ? 1 : 0};
   }
-  const dim3 grid(P.segs, g.BH, count);
   const int hold = debug_withhold(g, SLA_WITHHOLD_SUMMARIES) ? 1 : 0;
-  float* s1 = jobs[count - 1].sums;
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, smem, s>>>(m[0], m[1], m[2], m[3], log_decay, lens, jobs[0].sums, s1, P, r[0],
-                                      r[1], status, zero, wait_limit(g), hold);
+    kern<<<dim3(P.parts, count), kThreads, smem, s>>>(m[0], m[1], m[2], m[3], log_decay, lens, jobs[0].sums,
+                                                      jobs[count - 1].sums, P, r[0], r[1], status, zero,
+                                                      wait_limit(g), hold);
     return cudaGetLastError();
   };
   return g.d == 128 ? go(decay_sums_tc<128>, SumsSmem<128>::total) : go(decay_sums_tc<64>, SumsSmem<64>::total);
 }
 
 cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, const float* log_decay,
-                                const int32_t* lens, const float* starts, i64 start_stride, void* out,
-                                const DecayPlan& P, const DecayRole& R, const Geom& g, int32_t* status,
+                                const int32_t* lens, const DecayStart& start, void* out,
+                                const DecayParts& P, const DecayRole& R, const Geom& g, int32_t* status,
                                 int32_t* zero, cudaStream_t s) {
-  CUtensorMap ma, mb, mc;
-  if (!token_map(&ma, a, g) || !token_map(&mb, b, g) || !token_map(&mc, c, g)) return cudaErrorInvalidValue;
+  CUtensorMap ma, mb, mc, mo;
+  if (!token_map(&ma, a, g, kC) || !token_map(&mb, b, g, kC) || !token_map(&mc, c, g, kC) ||
+      !token_map(&mo, out, g, kC))
+    return cudaErrorInvalidValue;
   const int hold = debug_withhold(g, SLA_WITHHOLD_ATTENTION) ? 1 : 0;
+  const int d = g.d;
+  StateView v{start.state, i64(d) * d, start.packed, 0, 0, 0, 0};
+  if (start.packed && !R.transposed) v.r4 = 16, v.r1 = 4, v.c4 = 4 * d, v.c1 = 1;
+  if (start.packed && R.transposed) v.r4 = 4 * d, v.r1 = 1, v.c4 = 16, v.c1 = 4;
+  if (!start.packed && !R.transposed) v.r4 = 4 * d, v.r1 = d, v.c4 = 4, v.c1 = 1;
+  if (!start.packed && R.transposed) v.r4 = 4, v.r1 = 1, v.c4 = 4 * d, v.c1 = d;
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(P.segs, g.BH), kThreads, smem, s>>>(ma, mb, mc, log_decay, lens, starts, start_stride,
-                                                    static_cast<__nv_bfloat16*>(out), P, R, status, zero,
-                                                    wait_limit(g), hold);
+    kern<<<P.parts, kThreads, smem, s>>>(ma, mb, mc, mo, log_decay, lens, v, static_cast<__nv_bfloat16*>(out),
+                                         P, R, status, zero, wait_limit(g), hold);
     return cudaGetLastError();
   };
   if (g.d == 128)

@@ -265,7 +265,19 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
                                   const Geom& g, int32_t* zero, cudaStream_t s);
 // on the tensor cores (decay_tc.cu); a launch sums one or two jobs
 bool decay_tc_supported(const Geom& g);
-int decay_tc_chunk();
+// The heads' chunks of 128 tokens, in order, are dealt out evenly: CTA k of
+// `parts` takes [begin(k), begin(k + 1)), which heads' ends cut into pieces.
+// Piece (k, bh) has place k + bh in the workspace of sums.
+struct DecayParts {
+  int N, H;
+  int chunks, parts;  // chunks per head
+  i64 total;          // of all heads
+#ifdef __CUDACC__
+  __host__ __device__
+#endif
+  i64 begin(int k) const { return total * k / parts; }
+};
+DecayParts decay_parts(const Geom& g);
 struct DecaySums {
   const void *b, *c;
   float* sums;
@@ -274,15 +286,26 @@ struct DecaySums {
   bool reverse;
 };
 cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* log_decay,
-                                 const int32_t* lens, const DecayPlan& P, const Geom& g,
+                                 const int32_t* lens, const DecayParts& P, const Geom& g,
                                  int32_t* status, int32_t* zero, cudaStream_t s);
+// The state at each piece's entering side: the sums' workspace after the
+// scan (packed: units of 4 columns, rows adjacent), or one row-major [d, d]
+// per head; null: zeros.
+struct DecayStart {
+  const float* state;
+  bool packed;
+};
 cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, const float* log_decay,
-                                const int32_t* lens, const float* starts, i64 start_stride, void* out,
-                                const DecayPlan& P, const DecayRole& R, const Geom& g, int32_t* status,
+                                const int32_t* lens, const DecayStart& start, void* out,
+                                const DecayParts& P, const DecayRole& R, const Geom& g, int32_t* status,
                                 int32_t* zero, cudaStream_t s);
 cudaError_t launch_decay_scan(float* sums, const float* first, float* final_state,
                               const float* log_decay, const int32_t* lens, const DecayPlan& P,
                               bool reverse, const Geom& g, cudaStream_t s);
+// the same over pieces, packed sums; `turned`: `first` is their transpose
+cudaError_t launch_decay_scan_parts(float* sums, const float* first, bool turned, float* final_state,
+                                    const float* log_decay, const int32_t* lens, const DecayParts& P,
+                                    bool reverse, const Geom& g, cudaStream_t s);
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                               const int32_t* lens, const float* state_in, float* state_out, void* out,
                               const Geom& g, int32_t* zero, cudaStream_t s);

@@ -173,10 +173,10 @@ BwdWs bwd_ws(const Geom& g) {
   return w;
 }
 
-// Segments of the decayed linear attention: enough (head, segment) pairs for
-// two waves of one CTA per SM, whole chunks each.
+// Segments of the fp32 kernels of the decayed linear attention: enough (head,
+// segment) pairs for two waves of one CTA per SM, whole chunks each.
 sla::DecayPlan decay_plan(const Geom& g) {
-  const int chunk = sla::decay_tc_supported(g) ? sla::decay_tc_chunk() : sla::decay_simt_chunk();
+  const int chunk = sla::decay_simt_chunk();
   const int chunks = (g.N + chunk - 1) / chunk;
   const int want = std::min(chunks, std::max(1, (2 * 148 + g.BH - 1) / g.BH));
   sla::DecayPlan P;
@@ -188,15 +188,27 @@ sla::DecayPlan decay_plan(const Geom& g) {
 }
 
 DecayWs decay_ws(const Geom& g, bool backward) {
-  const sla::DecayPlan P = decay_plan(g);
-  const bool sums = P.segs > 1 || sla::decay_tc_supported(g);
-  const size_t states = sums ? sizeof(float) * size_t(g.BH) * P.segs * g.d * g.d : 0;
+  size_t states;  // in the workspace of one set of sums
+  if (sla::decay_tc_supported(g)) {
+    states = size_t(sla::decay_parts(g).parts) + g.BH;
+  } else {
+    const sla::DecayPlan P = decay_plan(g);
+    states = P.segs > 1 ? size_t(g.BH) * P.segs : 0;
+  }
+  states *= sizeof(float) * g.d * g.d;
   DecayWs w;
   size_t off = kStatusBytes;
   w.sums = off; off = align_up(off + states);
   w.rsums = off; if (backward) off = align_up(off + states);
   w.total = off;
   return w;
+}
+
+// Whether no part of the chunks cuts a head.
+bool whole_heads(const sla::DecayParts& P) {
+  for (int k = 1; k < P.parts; ++k)
+    if (P.begin(k) % P.chunks) return false;
+  return true;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -793,32 +805,31 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     SLA_CUDA(sla::launch_decay_step(q, k, v, log_decay, lens, state_in, state_out, out, g, status, s));
     return SLA_OK;
   }
-  const sla::DecayPlan P = decay_plan(g);
   const sla::DecayRole R{g.scale, g.scale, 1.0f, 0, false, false};
+  float* sums = at<float>(ws, w.sums);
   if (sla::decay_tc_supported(g)) {
-    // the state that is handed on comes from the sums kernel, which keeps it
-    // to fp32 accuracy; one segment and no state wanted need no sums
-    float* sums = at<float>(ws, w.sums);
-    const float* starts = state_in;
-    int64_t stride = int64_t(g.d) * g.d;
+    // the state that is handed on, to the next piece of a head or to the
+    // caller, comes from the sums kernel, which keeps it to fp32 accuracy;
+    // whole heads and no state wanted need no sums
+    const sla::DecayParts P = sla::decay_parts(g);
+    sla::DecayStart start{state_in, false};
     int32_t* zero = status;
-    if (P.segs > 1 || state_out) {
+    if (!whole_heads(P) || state_out) {
       const sla::DecaySums job{k, v, sums, 1.0f, 0, false};
       SLA_CUDA(sla::launch_decay_sums_tc(&job, 1, log_decay, lens, P, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan(sums, state_in, state_out, log_decay, lens, P, false, g, s));
-      starts = sums;
-      stride *= P.segs;
+      SLA_CUDA(sla::launch_decay_scan_parts(sums, state_in, false, state_out, log_decay, lens, P, false, g, s));
+      start = {sums, true};
       zero = nullptr;
     }
-    SLA_CUDA(sla::launch_decay_out_tc(q, k, v, log_decay, lens, starts, stride, out, P, R, g, status, zero, s));
+    SLA_CUDA(sla::launch_decay_out_tc(q, k, v, log_decay, lens, start, out, P, R, g, status, zero, s));
     return SLA_OK;
   }
+  const sla::DecayPlan P = decay_plan(g);
   if (P.segs == 1) {
     SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, state_in, int64_t(g.d) * g.d, out,
                                         state_out, P, R, g, status, s));
     return SLA_OK;
   }
-  float* sums = at<float>(ws, w.sums);
   SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
   SLA_CUDA(sla::launch_decay_scan(sums, state_in, state_out, log_decay, lens, P, false, g, s));
   SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, sums, int64_t(P.segs) * g.d * g.d, out,
@@ -858,37 +869,39 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
   if (ws_bytes < w.total) return SLA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t* status = at<int32_t>(ws, 0);
-  const sla::DecayPlan P = decay_plan(g);
   const sla::DecayRole Rq{g.scale, g.scale, 1.0f, 0, false, true};
   const sla::DecayRole Rv{g.scale, 1.0f, g.scale, 1, true, false};
   const sla::DecayRole Rk{g.scale, 1.0f, g.scale, 1, true, true};
+  if (sla::decay_tc_supported(g)) {
+    const sla::DecayParts P = sla::decay_parts(g);
+    float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
+    int32_t* zero = status;
+    // S^T for dq (b, c = v, k), R for dv and, read across, for dk
+    const sla::DecaySums jobs[2] = {{q, dout, rsums, g.scale, 1, true}, {v, k, sums, 1.0f, 0, false}};
+    const bool need_s = !whole_heads(P), need_r = need_s || dstate_in;
+    sla::DecayStart s_start{state_in, false}, r_start{dstate_out, false};
+    sla::DecayRole Rs = Rq;
+    if (need_r) {
+      SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, P, g, status, zero, s));
+      SLA_CUDA(sla::launch_decay_scan_parts(rsums, dstate_out, false, dstate_in, log_decay, lens, P, true, g, s));
+      r_start = {rsums, true};
+      zero = nullptr;
+    }
+    if (need_s) {
+      SLA_CUDA(sla::launch_decay_scan_parts(sums, state_in, true, nullptr, log_decay, lens, P, false, g, s));
+      s_start = {sums, true};
+      Rs.transposed = false;
+    }
+    SLA_CUDA(sla::launch_decay_out_tc(dout, v, k, log_decay, lens, s_start, dq, P, Rs, g, status, zero, s));
+    SLA_CUDA(sla::launch_decay_out_tc(v, dout, q, log_decay, lens, r_start, dk, P, Rk, g, status, nullptr, s));
+    SLA_CUDA(sla::launch_decay_out_tc(k, q, dout, log_decay, lens, r_start, dv, P, Rv, g, status, nullptr, s));
+    return SLA_OK;
+  }
+  const sla::DecayPlan P = decay_plan(g);
   const int64_t one = int64_t(g.d) * g.d;
   const float *s0 = state_in, *r0 = dstate_out;
   int64_t stride = one;
   float* fin = dstate_in;
-  if (sla::decay_tc_supported(g)) {
-    float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
-    int32_t* zero = status;
-    int64_t rstride = one;
-    const sla::DecaySums jobs[2] = {{q, dout, rsums, g.scale, 1, true}, {k, v, sums, 1.0f, 0, false}};
-    const bool need_s = P.segs > 1, need_r = P.segs > 1 || dstate_in;
-    if (need_r) {
-      SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, P, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan(rsums, dstate_out, dstate_in, log_decay, lens, P, true, g, s));
-      r0 = rsums;
-      rstride = P.segs * one;
-      zero = nullptr;
-    }
-    if (need_s) {
-      SLA_CUDA(sla::launch_decay_scan(sums, state_in, nullptr, log_decay, lens, P, false, g, s));
-      s0 = sums;
-      stride = P.segs * one;
-    }
-    SLA_CUDA(sla::launch_decay_out_tc(dout, v, k, log_decay, lens, s0, stride, dq, P, Rq, g, status, zero, s));
-    SLA_CUDA(sla::launch_decay_out_tc(v, dout, q, log_decay, lens, r0, rstride, dk, P, Rk, g, status, nullptr, s));
-    SLA_CUDA(sla::launch_decay_out_tc(k, q, dout, log_decay, lens, r0, rstride, dv, P, Rv, g, status, nullptr, s));
-    return SLA_OK;
-  }
   if (P.segs > 1) {
     float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
     SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
