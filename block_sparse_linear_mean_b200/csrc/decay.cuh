@@ -10,11 +10,13 @@ namespace sla {
 #ifdef __CUDACC__
 // decay^n = 2^(n log2 e log_decay); -inf is a decay of zero.  The exponent is
 // formed and reduced in 64 bits: in 32 its rounding alone would put powers of
-// a few hundred tokens off by 2^-20, the same way for every element.
+// a few hundred tokens off by 2^-20, the same way for every element.  (Not
+// inlined: the tensor-core kernels' warps already run six programs side by
+// side, and the instruction cache has to hold them.)
 __device__ __forceinline__ double decay_log2(float log_decay) {
   return static_cast<double>(log_decay) * 1.4426950408889634074;
 }
-__device__ __forceinline__ float decay_power(double l2, int n) {
+static __device__ __noinline__ float decay_power(double l2, int n) {
   if (n == 0) return 1.f;
   const double x = fmax(static_cast<double>(n) * l2, -1e6);
   const double i = rint(x);
@@ -23,7 +25,7 @@ __device__ __forceinline__ float decay_power(double l2, int n) {
 // The same as an unevaluated sum of two floats, for factors that are applied
 // again and again (a chunk's, a segment's): their error grows with the number
 // of times.
-__device__ __forceinline__ float2 decay_power2(double l2, int n) {
+static __device__ __noinline__ float2 decay_power2(double l2, int n) {
   if (n == 0) return make_float2(1.f, 0.f);
   const double p = exp2(static_cast<double>(n) * l2);
   const float hi = static_cast<float>(p);

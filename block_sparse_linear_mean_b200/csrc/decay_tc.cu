@@ -36,11 +36,15 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
 }
 
 // All waits of a CTA: bounded, and given up as soon as another warp has.
+// (Only the first try is inlined: the warps of a CTA run six programs side by
+// side, and with every wait unrolled the code outgrew the instruction cache,
+// which SMs share: the larger their group, the slower they ran, 71 to 103 us
+// of the same work.)
 struct Waiter {
   int32_t* status;
   volatile int* abort_flag;
   long long limit;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+  __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const {
     const long long t0 = clock64();
     for (uint32_t it = 0;; ++it) {
       if (mbar_try_wait(bar, parity)) return true;
@@ -53,6 +57,9 @@ struct Waiter {
         }
       }
     }
+  }
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    return mbar_try_wait(bar, parity) || slow(bar, parity);
   }
 };
 
@@ -91,6 +98,43 @@ __device__ __forceinline__ Piece<T> get_piece(const DecayParts& P, const int32_t
   x.tokens = min(max(decay_tokens(lens, bh / P.H, P.N) - x.t0, 0), x.cap);
   x.count = (x.tokens + T - 1) / T;
   x.reverse = reverse;
+  return x;
+}
+
+// The issuer's whole warp runs its program and one lane is elected at each
+// product.  Control flow and operands are then the same for all lanes as far
+// as the compiler can see (votes and reductions below say so where it could
+// not), and descriptors are formed in uniform registers: issued from a branch
+// that only one lane takes, a product costs that lane 110 to 140 cycles, twice
+// what it takes on the tensor core.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync t|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync t|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b32 t;\n\telect.sync t|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+template <int T>
+__device__ __forceinline__ Piece<T> uniform(Piece<T> x) {
+  x.t0 = uniform(x.t0);
+  x.tokens = uniform(x.tokens);
+  x.count = uniform(x.count);
   return x;
 }
 
@@ -175,8 +219,8 @@ struct SumsSmem {
   static constexpr int stages = 6;
   static constexpr uint32_t off_eye = stages * stage;
   static constexpr uint32_t off_bar = off_eye + kEyeBytes;
-  static constexpr uint32_t off_tab = off_bar + 256;
-  static constexpr uint32_t used = off_tab + 1024;
+  static constexpr uint32_t off_tab = off_bar + 256;       // of both groups: 64 weights, 64 zeros
+  static constexpr uint32_t used = off_tab + 1024 + 1024;
   static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM
 };
 
@@ -252,75 +296,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 17) {
-    if (tid % 32 == 0) {
-      constexpr uint32_t id_t = idesc_bf16(128, 16, 1, 0), id_s = idesc_bf16(128, D, 0, 1);
-      const uint64_t eye = eye_desc(sb + L::off_eye);
-      int s = 0, ph = 0;          // stage of the next T
-      uint32_t clears = 0;        // bit q: parity of group q's next clearing
-      // T of step j (of `size` tokens) into buffer j & 1
-      auto issue_t = [&](int j, int size) -> bool {
-        if (!wait(b_full + 8 * s, ph)) return false;
-        if (size < kT) {
-          if (!wait(b_clear + 8 * (j & 1), clears >> (j & 1) & 1)) return false;
-          clears ^= 1u << (j & 1);
-        }
-        tc_fence_after();
-        // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
-        const uint64_t db = sdesc(sb + s * L::stage, L::half, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)
-          tc_mma(tmem + 128 * (j & 1) + 16 * kk, sdesc_add(db, kk * 2048), eye, id_t, 0u);
-        tc_commit(b_t + 8 * (j & 1));
-        if (++s == L::stages) { s = 0; ph ^= 1; }
-        return true;
-      };
-      int j = 0, m = 0, sm = 0;  // step, accumulation, stage of the products
-      Piece<kT> pc = get_piece<kT>(P, lens, part, bh0, rev);
-      int bh = bh0, i = 0;
-      while (bh <= bh1 && pc.count == 0) {
-        if (++bh <= bh1) pc = get_piece<kT>(P, lens, part, bh, rev);
+    constexpr uint32_t id_t = idesc_bf16(128, 16, 1, 0), id_s = idesc_bf16(128, D, 0, 1);
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+    const uint64_t eye = eye_desc(sb + L::off_eye), db0 = sdesc(sb, L::half, 1024),
+                   dc0 = sdesc(sb + L::tile, L::half, 1024);
+    int s = 0, ph = 0;          // stage of the next T
+    uint32_t clears = 0;        // bit q: parity of group q's next clearing
+    // T of step j (of `size` tokens) into buffer j & 1
+    auto issue_t = [&](int j, int size) -> bool {
+      if (!__all_sync(all, wait(b_full + 8 * s, ph))) return false;
+      if (size < kT) {
+        if (!__all_sync(all, wait(b_clear + 8 * (j & 1), clears >> (j & 1) & 1))) return false;
+        clears ^= 1u << (j & 1);
       }
-      bool more = bh <= bh1;
-      if (more) ok = issue_t(0, pc.size(0));
-      while (ok && more) {
-        const int place = i % kFlush;
-        const bool end = place == kFlush - 1 || i + 1 == pc.count;
-        // the step behind this one
-        if (++i == pc.count) {
-          i = 0;
-          do {
-            if (++bh <= bh1) pc = get_piece<kT>(P, lens, part, bh, rev);
-          } while (bh <= bh1 && pc.count == 0);
-          more = bh <= bh1;
-        }
-        // (a partial one is cleared by workers that may be waiting, at a piece's
-        // end, for the products of this step: those go first then)
-        const bool ahead = more && pc.size(i) == kT;
-        if (ahead && !(ok = issue_t(j + 1, kT))) break;
-        const int q = j & 1;
-        if (place == 0 && m >= 2 && !(ok = wait(b_flush + 8 * (m & 1), ((m >> 1) & 1) ^ 1))) break;
-        if (!(ok = wait(b_ready + 8 * q, (j >> 1) & 1))) break;
-        tc_fence_after();
-        const uint32_t td = tmem + 256 + 128 * (m & 1), tp = tmem + 128 * q, first = place != 0 ? 1u : 0u;
-        const uint64_t dc = sdesc(sb + sm * L::stage + L::tile, L::half, 1024);
+      tc_fence_after();
+      // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
+      const uint64_t db = sdesc_add(db0, s * L::stage);
+      const uint32_t td = tm + 128 * (j & 1);
 #pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)  // lo2
-          tc_mma_ts(td, tp + 64 + kk * 8, sdesc_add(dc, kk * 2048), id_s, kk > 0 ? 1u : first);
-#pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)  // lo
-          tc_mma_ts(td, tp + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_s, 1u);
-#pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)  // hi
-          tc_mma_ts(td, tp + kk * 16, sdesc_add(dc, kk * 2048), id_s, 1u);
-        tc_commit(b_empty + 8 * sm);
-        if (end) {
-          tc_commit(b_acc + 8 * (m & 1));
-          ++m;
-        }
-        if (++sm == L::stages) sm = 0;
-        if (more && !ahead && !(ok = issue_t(j + 1, pc.size(i)))) break;
-        ++j;
+      for (int kk = 0; kk < kT / 16; ++kk) mma_ss(td + 16 * kk, sdesc_add(db, kk * 2048), eye, id_t, 0u);
+      mma_commit(b_t + 8 * (j & 1));
+      if (++s == L::stages) { s = 0; ph ^= 1; }
+      return true;
+    };
+    int j = 0, m = 0, sm = 0;  // step, accumulation, stage of the products
+    int bh = bh0, i = 0;
+    Piece<kT> pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
+    while (bh <= bh1 && pc.count == 0) {
+      if (++bh <= bh1) pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
+    }
+    bool more = bh <= bh1;
+    if (more) ok = issue_t(0, pc.size(0));
+    while (ok && more) {
+      const int place = i % kFlush;
+      const bool end = place == kFlush - 1 || i + 1 == pc.count;
+      // the step behind this one
+      if (++i == pc.count) {
+        i = 0;
+        do {
+          if (++bh <= bh1) pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
+        } while (bh <= bh1 && pc.count == 0);
+        more = bh <= bh1;
       }
+      // (a partial one is cleared by workers that may be waiting, at a piece's
+      // end, for the products of this step: those go first then)
+      const bool ahead = more && pc.size(i) == kT;
+      if (ahead && !(ok = issue_t(j + 1, kT))) break;
+      const int q = j & 1;
+      if (place == 0 && m >= 2 &&
+          !(ok = __all_sync(all, wait(b_flush + 8 * (m & 1), ((m >> 1) & 1) ^ 1)))) break;
+      if (!(ok = __all_sync(all, wait(b_ready + 8 * q, (j >> 1) & 1)))) break;
+      tc_fence_after();
+      const uint32_t td = tm + 256 + 128 * (m & 1), tp = tm + 128 * q, first = place != 0 ? 1u : 0u;
+      const uint64_t dc = sdesc_add(dc0, sm * L::stage);
+#pragma unroll
+      for (int kk = 0; kk < kT / 16; ++kk)  // lo2
+        mma_ts(td, tp + 64 + kk * 8, sdesc_add(dc, kk * 2048), id_s, kk > 0 ? 1u : first);
+#pragma unroll
+      for (int kk = 0; kk < kT / 16; ++kk)  // lo
+        mma_ts(td, tp + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_s, 1u);
+#pragma unroll
+      for (int kk = 0; kk < kT / 16; ++kk)  // hi
+        mma_ts(td, tp + kk * 16, sdesc_add(dc, kk * 2048), id_s, 1u);
+      mma_commit(b_empty + 8 * sm);
+      if (end) {
+        mma_commit(b_acc + 8 * (m & 1));
+        ++m;
+      }
+      if (++sm == L::stages) sm = 0;
+      if (more && !ahead && !(ok = issue_t(j + 1, pc.size(i)))) break;
+      ++j;
     }
   } else {
     const int quad = warp & 3, group = warp >> 3, h = warp >> 2 & 1;
@@ -357,19 +402,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const double l2 = decay_log2(log_decay[bh % P.H]);
       // the group's own table of decay^(place in a full step); every warp
       // comes here, also one whose wait gave up
-      float* tab = pw + 64 * group;
+      float* tab = pw + 2 * kT * group;
       if (!(ok = bar_sync_and(1 + group, 256, ok))) break;
-      if ((tid & 255) < kT) tab[tid & 255] = decay_power(l2, R.reverse ? tid & 255 : kT - 1 - (tid & 255));
+      const int k = tid & 255;
+      if (k < kT) tab[k] = decay_power(l2, R.reverse ? k : kT - 1 - k);
+      else if (k < 2 * kT) tab[k] = 0.f;
       asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory");
 #pragma unroll
       for (int x = 0; x < CW; ++x) acc[x] = 0.f;
+      // weight of a step's near edge, toward the leaving side: the steps come
+      // from there, so it falls by decay^64 each time (in 64 bits)
+      double far = R.w_sum * decay_power(l2, R.e);
+      const double fall = exp2(fmax(l2 * kT, -2000.0));
       for (int i = 0; ok && i < pc.count; ++i, ++j) {
         if ((j & 1) == group) {
-          const int nc = pc.size(i), row0 = pc.at(i) * kT;
-          // distance of the step's near edge from the leaving side: the table
-          // counts whole steps, and a partial one ends early (forward)
-          const int near = R.reverse ? row0 : pc.tokens - row0 - kT;
-          const float far_w = R.w_sum * decay_power(l2, max(near, 0) + R.e);
+          const int nc = pc.size(i);
+          const float far_w = static_cast<float>(far);
           const uint32_t tT = tmem + 128 * group + lane;
           if (nc < kT) {
             if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
@@ -386,19 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tT + 32 * h, v);
             tmem_wait_ld();
             reg_fence<32>(v);
-            const float2 fw = make_float2(far_w, far_w);
-            if (near >= 0) {
+            // the table counts whole steps; a partial one of the forward ends
+            // early on the near side
+            const float* w = tab + 32 * h + (R.reverse ? 0 : kT - nc);
 #pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(tab + 32 * h + x);
-                const float2 a = mul2(make_float2(v[x], v[x + 1]), mul2(fw, make_float2(w.x, w.y)));
-                const float2 b = mul2(make_float2(v[x + 2], v[x + 3]), mul2(fw, make_float2(w.z, w.w)));
-                v[x] = a.x; v[x + 1] = a.y; v[x + 2] = b.x; v[x + 3] = b.y;
-              }
-            } else {  // forward, partial: token nc - 1 is the near edge
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] *= far_w * tab[min(32 * h + x + kT - nc, kT - 1)];
-            }
+            for (int x = 0; x < 32; ++x) v[x] *= far_w * w[x];
             // the 16 columns read take hi and lo of their tokens
 #pragma unroll
             for (int c = 0; c < 32; c += 16) {
@@ -417,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (tid % 32 == 0) mbar_arrive(b_ready + 8 * group);
         }
+        far *= pc.size(i) == kT ? fall : exp2(l2 * pc.size(i));
         if (pending && !(ok = flush())) break;
         pending = i % kFlush == kFlush - 1 || i + 1 == pc.count;
         if (++s == L::stages) { s = 0; ph ^= 1; }
@@ -467,8 +508,8 @@ struct OutSmem {
   static constexpr uint32_t off_eye = off_s + s_bytes;
   static constexpr uint32_t off_bar = off_eye + kEyeBytes;
   static constexpr uint32_t off_wt = off_bar + 160;        // the tokens' weights in a chunk
-  static constexpr uint32_t off_tab = off_wt + 512;        // decay^k, k <= 128
-  static constexpr uint32_t used = off_tab + 132 * 4 + 1024;
+  static constexpr uint32_t off_tab = off_wt + 512;        // 32 zeros, then decay^k, k < 128
+  static constexpr uint32_t used = off_tab + 160 * 4 + 1024;
   // one CTA per SM: it takes all of tensor memory
   static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;
 };
@@ -551,65 +592,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 17) {
-    if (tid % 32 == 0) {
-      constexpr uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1),
-                         id_t = idesc_bf16(128, 16, 1, 0);
-      const uint64_t ds = sdesc(sb + L::off_s, D * 128, 1024), eye = eye_desc(sb + L::off_eye);
-      int j = 0, ju = 0, clears = 0;  // chunk; chunk that moves the state; partial chunk
-      for (int bh = bh0; ok && bh <= bh1; ++bh) {
-        const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
-        for (int i = 0; i < pc.count; ++i, ++j) {
-          const int s = j & 1;
-          const bool last = i + 1 == pc.count;
-          const uint32_t st = sb + s * L::stage;
-          const uint64_t da = sdesc(st, 16, 1024), db = sdesc(st + L::tile, 16, 1024),
-                         dbt = sdesc(st + L::tile, 16384, 1024), dc = sdesc(st + 2 * L::tile, 16384, 1024);
-          if (!(ok = wait(b_full + 8 * s, (j >> 1) & 1))) break;
-          if (pc.size(i) < kC && !(ok = wait(b_clear, clears++ & 1))) break;
-          tc_fence_after();
-          // X = a b^T, over the P that the products before have read
+    constexpr uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1),
+                       id_t = idesc_bf16(128, 16, 1, 0);
+    const uint32_t uX = static_cast<uint32_t>(uniform(static_cast<int>(tX))), uO = uX + 128, uU = uX + 256,
+                   uT = uX + 384;
+    const uint64_t ds = sdesc(sb + L::off_s, D * 128, 1024), eye = eye_desc(sb + L::off_eye),
+                   da0 = sdesc(sb, 16, 1024), dt0 = sdesc(sb, 16384, 1024);
+    int j = 0, ju = 0, clears = 0;  // chunk; chunk that moves the state; partial chunk
+    for (int bh = bh0; ok && bh <= bh1; ++bh) {
+      const Piece<kC> pc = uniform(get_piece<kC>(P, lens, part, bh, REV));
+      for (int i = 0; i < pc.count; ++i, ++j) {
+        const int s = j & 1;
+        const bool last = i + 1 == pc.count;
+        const uint64_t da = sdesc_add(da0, s * L::stage), db = sdesc_add(da, L::tile),
+                       dbt = sdesc_add(dt0, s * L::stage + L::tile), dc = sdesc_add(dbt, L::tile);
+        if (!(ok = __all_sync(all, wait(b_full + 8 * s, (j >> 1) & 1)))) break;
+        if (pc.size(i) < kC && !(ok = __all_sync(all, wait(b_clear, clears++ & 1)))) break;
+        tc_fence_after();
+        // X = a b^T, over the P that the products before have read
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            tc_mma(tX, sdesc_add(da, off), sdesc_add(db, off), id_x, kk > 0);
-          }
-          tc_commit(b_x);
-          if (!last) {  // (behind a piece's last chunk nobody reads the state)
-            // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) tc_mma(tT + 16 * kk, sdesc_add(dbt, kk * 2048), eye, id_t, 0u);
-            tc_commit(b_t);
-          }
-          // Z = a S
-          if (!(ok = wait(b_sr, j & 1))) break;
-          if (j > 0 && !(ok = wait(b_free, (j - 1) & 1))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma(tO, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_add(ds, kk * 2048), id_o, kk > 0);
-          tc_commit(b_z);
-          // U = (w b)^T c
-          if (!last) {
-            if (!(ok = wait(b_w, ju & 1))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_ts(tU, tT + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_o, kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_ts(tU, tT + kk * 16, sdesc_add(dc, kk * 2048), id_o, 1u);
-            tc_commit(b_u);
-            ++ju;
-          }
-          // O = scaled Z + P c
-          if (!(ok = wait(b_p, j & 1) && wait(b_zs, j & 1))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts(tO, tX + kk * 8, sdesc_add(dc, kk * 2048), id_o, 1u);
-          tc_commit(b_o);
-          tc_commit(b_ebc + 8 * s);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_ss(uX, sdesc_add(da, off), sdesc_add(db, off), id_x, kk > 0);
         }
+        mma_commit(b_x);
+        if (!last) {  // (behind a piece's last chunk nobody reads the state)
+          // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ss(uT + 16 * kk, sdesc_add(dbt, kk * 2048), eye, id_t, 0u);
+          mma_commit(b_t);
+        }
+        // Z = a S
+        if (!(ok = __all_sync(all, wait(b_sr, j & 1)))) break;
+        if (j > 0 && !(ok = __all_sync(all, wait(b_free, (j - 1) & 1)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(uO, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_add(ds, kk * 2048), id_o, kk > 0);
+        mma_commit(b_z);
+        // U = (w b)^T c
+        if (!last) {
+          if (!(ok = __all_sync(all, wait(b_w, ju & 1)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts(uU, uT + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_o, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts(uU, uT + kk * 16, sdesc_add(dc, kk * 2048), id_o, 1u);
+          mma_commit(b_u);
+          ++ju;
+        }
+        // O = scaled Z + P c
+        if (!(ok = __all_sync(all, wait(b_p, j & 1) && wait(b_zs, j & 1)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ts(uO, uX + kk * 8, sdesc_add(dc, kk * 2048), id_o, 1u);
+        mma_commit(b_o);
+        mma_commit(b_ebc + 8 * s);
       }
     }
   } else if (warp < 4) {
@@ -619,35 +657,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
       // (every warp comes here, also one whose wait gave up)
       if (!(ok = bar_sync_and(1, 128, ok))) break;
-      pw[r] = R.w_in * decay_power(decay_log2(log_decay[bh % P.H]), r);
+      pw[32 + r] = R.w_in * decay_power(decay_log2(log_decay[bh % P.H]), r);
+      if (r < 32) pw[r] = 0.f;  // pairs that the mask leaves out: gaps -32 .. -1
       asm volatile("bar.sync 1, 128;" ::: "memory");
       for (int i = 0; ok && i < pc.count; ++i, ++j) {
-        const int nc = pc.size(i);
         if (!(ok = __all_sync(all, wait(b_x, j & 1)))) break;
         tc_fence_after();
-#pragma unroll
+        // blocks of 32 columns: before (behind) all of the warp's rows full,
+        // on the diagonal masked by the table, the others empty
+#pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
           uint32_t pk[16];
-          // a block of 32 columns before (behind) all of the warp's rows is
-          // full, one behind (before) them empty, the one on the diagonal mixed
-          const bool empty = REV ? cb < quad : cb > quad;
-          if (empty) {
+          if (REV ? cb < quad : cb > quad) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0u;
           } else {
             float v[32];
             tmem_ld32(tX + lane + cb * 32, v);
+            const float* w = pw + 32 + (REV ? cb * 32 - r : r - cb * 32);
             tmem_wait_ld();
             reg_fence<32>(v);
-            const bool mixed = cb == quad || (REV && nc < kC);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int jj = cb * 32 + x, gap = REV ? jj - r : r - jj;
-              const bool in = !mixed || (gap >= 0 && (!REV || jj < nc));
-              v[x] = in ? v[x] * pw[in ? gap : 0] : 0.f;
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) pk[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+            for (int x = 0; x < 16; ++x)
+              pk[x] = REV ? pack_bf16x2(v[2 * x] * w[2 * x], v[2 * x + 1] * w[2 * x + 1])
+                          : pack_bf16x2(v[2 * x] * w[-2 * x], v[2 * x + 1] * w[-2 * x - 1]);
           }
           tmem_st16u(tX + lane + cb * 16, pk);
         }
@@ -707,18 +740,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = __all_sync(all, wait(b_t, ju & 1)))) break;
         tc_fence_after();
         if (mine) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
             float v[16];
             uint32_t p[8];
             const uint32_t t = tT + lane + 64 * h + c;
             tmem_ld16(t, v);
+            float4 w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const float4*>(wt + 64 * h + c + 4 * x);
             tmem_wait_ld();
             reg_fence<16>(v);
 #pragma unroll
-            for (int x = 0; x < 16; x += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(wt + 64 * h + c + x);
-              v[x] *= w.x; v[x + 1] *= w.y; v[x + 2] *= w.z; v[x + 3] *= w.w;
+            for (int x = 0; x < 4; ++x) {
+              v[4 * x] *= w[x].x; v[4 * x + 1] *= w[x].y;
+              v[4 * x + 2] *= w[x].z; v[4 * x + 3] *= w[x].w;
             }
             // the 16 columns read take hi and lo of their tokens
             take_part(v, p);
@@ -773,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && (ok = __all_sync(all, wait(b_z, j & 1)))) {
           tc_fence_after();
           const float2 ff = make_float2(f, f);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float z[32];
             tmem_ld32(tO + lane + c, z);
@@ -794,25 +830,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && (ok = __all_sync(all, wait(b_o, j & 1)))) {
           tc_fence_after();
-          uint32_t w[D / 2];
-#pragma unroll
+          // all products that read this a tile are complete
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
             tmem_ld32(tO + lane + c, o);
             tmem_wait_ld();
             reg_fence<32>(o);
+            if (c + 32 == D) {  // the next Z may come over O
+              tc_fence_before();
+              __syncwarp();
+              if (tid % 32 == 0) mbar_arrive(b_free);
+            }
+            uint8_t* to = at + (c >> 6) * 16384;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) w[c / 2 + x] = real ? pack_bf16x2(o[2 * x], o[2 * x + 1]) : 0u;
+            for (int x = 0; x < 4; ++x) {
+              uint4 y = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                                   pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+              if (!real) y = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(to + sw128(r, ((c >> 3) & 7) + x)) = y;
+            }
           }
-          // the next Z may come over O
-          tc_fence_before();
-          __syncwarp();
-          if (tid % 32 == 0) mbar_arrive(b_free);
-          // all products that read this a tile are complete
-#pragma unroll
-          for (int u = 0; u < D / 8; ++u)
-            *reinterpret_cast<uint4*>(at + (u >> 3) * 16384 + sw128(r, u & 7)) =
-                make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
           fence_async_smem();
         }
         // (every warp comes here, also one whose wait gave up)
