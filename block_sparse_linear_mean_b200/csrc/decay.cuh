@@ -41,6 +41,31 @@ __device__ __forceinline__ int decay_tokens(const int32_t* lens, int b, int N) {
 __device__ __forceinline__ int segment_tokens(const DecayPlan& P, const int32_t* lens, int b, int seg) {
   return min(max(decay_tokens(lens, b, P.N) - seg * P.seg_len, 0), P.seg_len);
 }
+
+// A call's kernels follow one another without the launch's gap: each lets the
+// next one's CTAs start as SMs come free and waits, before it touches memory,
+// for all of the one before.  (The first kernel of a call is launched plainly,
+// behind whatever the stream holds.)
+__device__ __forceinline__ void next_may_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... A, typename... B>
+cudaError_t launch_behind(bool behind, void (*kern)(A...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t s, B... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, static_cast<A>(args)...);
+}
 #endif
 
 }  // namespace sla

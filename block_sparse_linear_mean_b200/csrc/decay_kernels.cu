@@ -247,14 +247,14 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
 //
 // The segments are the uniform ones of the fp32 kernels, or the pieces of the
 // tensor-core kernels with their packed sums (units of 4 columns, rows
-// adjacent).
+// adjacent).  Each block first tables its head's segments: place and factor.
 struct UniformSegments {
   DecayPlan P;
   static constexpr bool packed = false;
+  __device__ int first(int) const { return 0; }
   __device__ int count(int) const { return P.segs; }
-  __device__ int tokens_before(int, int i) const { return i * P.seg_len; }
-  __device__ int cap(int, int) const { return P.seg_len; }
-  __device__ i64 place(int bh, int i) const { return i64(bh) * P.segs + i; }
+  __device__ int begin(int, int i) const { return i * P.seg_len; }
+  __device__ int place(int bh, int i) const { return bh * P.segs + i; }
 };
 struct PieceSegments {
   DecayParts P;
@@ -263,60 +263,66 @@ struct PieceSegments {
   __device__ int part(i64 g) const { return static_cast<int>(((g + 1) * P.parts - 1) / P.total); }
   __device__ int first(int bh) const { return part(i64(bh) * P.chunks); }
   __device__ int count(int bh) const { return part(i64(bh + 1) * P.chunks - 1) - first(bh) + 1; }
-  __device__ int tokens_before(int bh, int i) const {
-    return static_cast<int>(max(P.begin(first(bh) + i) - i64(bh) * P.chunks, i64(0))) * 128;
+  // first token of part k within head bh
+  __device__ int begin(int bh, int k) const {
+    return static_cast<int>(min(max(P.begin(k) - i64(bh) * P.chunks, i64(0)), i64(P.chunks))) * 128;
   }
-  __device__ int cap(int bh, int i) const {
-    return static_cast<int>(min(P.begin(first(bh) + i + 1) - i64(bh) * P.chunks, i64(P.chunks))) * 128 -
-           tokens_before(bh, i);
-  }
-  __device__ i64 place(int bh, int i) const { return i64(first(bh)) + i + bh; }
+  __device__ int place(int bh, int k) const { return k + bh; }
 };
 
-constexpr int kScan = 14;  // segments' sums in flight per thread
+constexpr int kScan = 14;      // segments' sums in flight per thread
+constexpr int kScanTable = 512;  // segments of a head tabled at a time
 template <typename Segments>
-__global__ void __launch_bounds__(128) decay_scan_kernel(float4* __restrict__ sums, const float* first,
-                                                         bool turned, float4* final_state,
+__global__ void __launch_bounds__(128) decay_scan_kernel(DecayScanJob j0, DecayScanJob j1,
                                                          const float* __restrict__ log_decay,
                                                          const int32_t* __restrict__ lens, Segments G,
-                                                         int d, bool reverse) {
+                                                         int d) {
+  next_may_launch();
+  __shared__ float2 factor[kScanTable];
+  __shared__ int place[kScanTable];
+  const DecayScanJob J = blockIdx.z ? j1 : j0;
+  float4* sums = reinterpret_cast<float4*>(J.sums);
   const int dd4 = d * d / 4;
   const int u = blockIdx.x * 128 + threadIdx.x;
   const int bh = blockIdx.y;
-  if (u >= dd4) return;
   const int r = G.packed ? u % d : u / (d / 4), c = G.packed ? u / d * 4 : u % (d / 4) * 4;
   const double l2 = decay_log2(log_decay[bh % G.P.H]);
   const int len = decay_tokens(lens, bh / G.P.H, G.P.N);
-  const int segs = G.count(bh);
+  const int segs = G.count(bh), seg0 = G.first(bh);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (first) {
-    const float* f = first + i64(bh) * d * d;
-    s = turned ? make_float4(f[c * d + r], f[(c + 1) * d + r], f[(c + 2) * d + r], f[(c + 3) * d + r])
-               : *reinterpret_cast<const float4*>(f + r * d + c);
+  if (J.first) {
+    const float* f = J.first + i64(bh) * d * d;
+    s = J.turned ? make_float4(f[c * d + r], f[(c + 1) * d + r], f[(c + 2) * d + r], f[(c + 3) * d + r])
+                 : *reinterpret_cast<const float4*>(f + r * d + c);
   }
-  int n0 = -1;  // tokens that f stands for: most segments have the same
-  float2 f = make_float2(1.f, 0.f);
-  for (int i0 = 0; i0 < segs; i0 += kScan) {
-    float4 x[kScan];
+  for (int t0 = 0; t0 < segs; t0 += kScanTable) {
+    const int tn = min(kScanTable, segs - t0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < tn; i += 128) {
+      const int k = seg0 + (J.reverse ? segs - 1 - (t0 + i) : t0 + i);
+      const int b0 = G.begin(bh, k), b1 = G.begin(bh, k + 1);
+      factor[i] = decay_power2(l2, min(max(len - b0, 0), b1 - b0));
+      place[i] = G.place(bh, k);
+    }
+    __syncthreads();
+    if (t0 == 0) wait_for_previous();
+    for (int i0 = 0; i0 < tn; i0 += kScan) {
+      float4 x[kScan];
 #pragma unroll
-    for (int i = 0; i < kScan; ++i)
-      if (i0 + i < segs) x[i] = sums[G.place(bh, reverse ? segs - 1 - (i0 + i) : i0 + i) * dd4 + u];
+      for (int i = 0; i < kScan; ++i)
+        if (i0 + i < tn) x[i] = sums[i64(place[i0 + i]) * dd4 + u];
 #pragma unroll
-    for (int i = 0; i < kScan; ++i) {
-      if (i0 + i < segs) {
-        const int seg = reverse ? segs - 1 - (i0 + i) : i0 + i;
-        sums[G.place(bh, seg) * dd4 + u] = s;
-        const int n = min(max(len - G.tokens_before(bh, seg), 0), G.cap(bh, seg));
-        if (n != n0) {
-          f = decay_power2(l2, n);
-          n0 = n;
+      for (int i = 0; i < kScan; ++i) {
+        if (i0 + i < tn) {
+          sums[i64(place[i0 + i]) * dd4 + u] = s;
+          const float2 f = factor[i0 + i];
+          s.x = fmaf(f.x, s.x, fmaf(f.y, s.x, x[i].x)); s.y = fmaf(f.x, s.y, fmaf(f.y, s.y, x[i].y));
+          s.z = fmaf(f.x, s.z, fmaf(f.y, s.z, x[i].z)); s.w = fmaf(f.x, s.w, fmaf(f.y, s.w, x[i].w));
         }
-        s.x = fmaf(f.x, s.x, fmaf(f.y, s.x, x[i].x)); s.y = fmaf(f.x, s.y, fmaf(f.y, s.y, x[i].y));
-        s.z = fmaf(f.x, s.z, fmaf(f.y, s.z, x[i].z)); s.w = fmaf(f.x, s.w, fmaf(f.y, s.w, x[i].w));
       }
     }
   }
-  if (final_state) final_state[i64(bh) * dd4 + r * (d / 4) + c / 4] = s;
+  if (J.last) reinterpret_cast<float4*>(J.last)[i64(bh) * dd4 + r * (d / 4) + c / 4] = s;
 }
 
 // Few tokens: the state is read and written once, by CTAs that own 32 columns
@@ -445,22 +451,17 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
                    : out_simt<bf, 128>(x, y, z, log_decay, lens, starts, start_stride, o, final_state, P, R, g.BH, zero, s);
 }
 
-cudaError_t launch_decay_scan(float* sums, const float* first, float* final_state,
-                              const float* log_decay, const int32_t* lens, const DecayPlan& P,
-                              bool reverse, const Geom& g, cudaStream_t s) {
-  decay_scan_kernel<<<dim3(g.d * g.d / 512, g.BH), 128, 0, s>>>(
-      reinterpret_cast<float4*>(sums), first, false, reinterpret_cast<float4*>(final_state), log_decay,
-      lens, UniformSegments{P}, g.d, reverse);
-  return cudaGetLastError();
+cudaError_t launch_decay_scan(const DecayScanJob& job, const float* log_decay, const int32_t* lens,
+                              const DecayPlan& P, const Geom& g, cudaStream_t s) {
+  return launch_behind(false, decay_scan_kernel<UniformSegments>, dim3(g.d * g.d / 512, g.BH), 128, 0, s,
+                       job, job, log_decay, lens, UniformSegments{P}, g.d);
 }
 
-cudaError_t launch_decay_scan_parts(float* sums, const float* first, bool turned, float* final_state,
-                                    const float* log_decay, const int32_t* lens, const DecayParts& P,
-                                    bool reverse, const Geom& g, cudaStream_t s) {
-  decay_scan_kernel<<<dim3(g.d * g.d / 512, g.BH), 128, 0, s>>>(
-      reinterpret_cast<float4*>(sums), first, turned, reinterpret_cast<float4*>(final_state), log_decay,
-      lens, PieceSegments{P}, g.d, reverse);
-  return cudaGetLastError();
+cudaError_t launch_decay_scan_parts(const DecayScanJob* jobs, int count, const float* log_decay,
+                                    const int32_t* lens, const DecayParts& P, const Geom& g,
+                                    cudaStream_t s) {
+  return launch_behind(true, decay_scan_kernel<PieceSegments>, dim3(g.d * g.d / 512, g.BH, count), 128, 0,
+                       s, jobs[0], jobs[count - 1], log_decay, lens, PieceSegments{P}, g.d);
 }
 
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay,

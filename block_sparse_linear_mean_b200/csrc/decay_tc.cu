@@ -202,6 +202,7 @@ __device__ __forceinline__ void take_part(float* v, uint32_t* part) {
 // them, in turn) is added to fp32 registers, and within a step the small parts
 // go first.
 constexpr int kThreads = 576;      // 16 worker warps, loader, issuer
+constexpr int kSumThreads = 608;   // ... and two issuers
 constexpr int kT = 64;             // tokens per step
 constexpr int kFlush = 4;          // steps per accumulation
 
@@ -225,7 +226,7 @@ struct SumsSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kSumThreads, 1)
     decay_sums_tc(const __grid_constant__ CUtensorMap mb0, const __grid_constant__ CUtensorMap mc0,
                   const __grid_constant__ CUtensorMap mb1, const __grid_constant__ CUtensorMap mc1,
                   const float* __restrict__ log_decay, const int32_t* __restrict__ lens,
@@ -242,8 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_acc = smem_u32(bars + 16);    // [2] an accumulation is complete
   const uint32_t b_flush = smem_u32(bars + 18);  // [2] and has been read
   const uint32_t b_clear = smem_u32(bars + 20);  // [2] rows behind the end cleared, by group
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 22);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 23);
+  const uint32_t b_used = smem_u32(bars + 22);   // [2] parts multiplied
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 24);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 25);
   float* pw = reinterpret_cast<float*>(base + L::off_tab);  // decay^k by place in a step, per head parity
   const int tid = threadIdx.x, warp = tid / 32;
   const int part = blockIdx.x;
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b_acc + 8 * x, 1);
       mbar_init(b_flush + 8 * x, 16);
       mbar_init(b_clear + 8 * x, 8);
+      mbar_init(b_used + 8 * x, 1);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -273,6 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  next_may_launch();
+  wait_for_previous();
   // buffer q at 128 q: T at columns 0 .. 63, over 16 tokens' columns their hi
   // (8) and lo parts (8); lo2 at 64 .. 95.  Accumulators at 256 and 384
   const uint32_t tmem = *tslot;
@@ -296,76 +301,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 17) {
-    constexpr uint32_t id_t = idesc_bf16(128, 16, 1, 0), id_s = idesc_bf16(128, D, 0, 1);
+    // T of each step into the buffers in turn
+    constexpr uint32_t id_t = idesc_bf16(128, 16, 1, 0);
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
-    const uint64_t eye = eye_desc(sb + L::off_eye), db0 = sdesc(sb, L::half, 1024),
-                   dc0 = sdesc(sb + L::tile, L::half, 1024);
-    int s = 0, ph = 0;          // stage of the next T
+    const uint64_t eye = eye_desc(sb + L::off_eye), db0 = sdesc(sb, L::half, 1024);
+    int s = 0, ph = 0, j = 0;
     uint32_t clears = 0;        // bit q: parity of group q's next clearing
-    // T of step j (of `size` tokens) into buffer j & 1
-    auto issue_t = [&](int j, int size) -> bool {
-      if (!__all_sync(all, wait(b_full + 8 * s, ph))) return false;
-      if (size < kT) {
-        if (!__all_sync(all, wait(b_clear + 8 * (j & 1), clears >> (j & 1) & 1))) return false;
-        clears ^= 1u << (j & 1);
-      }
-      tc_fence_after();
-      // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
-      const uint64_t db = sdesc_add(db0, s * L::stage);
-      const uint32_t td = tm + 128 * (j & 1);
+    for (int bh = bh0; ok && bh <= bh1; ++bh) {
+      const Piece<kT> pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
+      for (int i = 0; i < pc.count; ++i, ++j) {
+        const int q = j & 1;
+        if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
+        if (pc.size(i) < kT) {
+          if (!(ok = __all_sync(all, wait(b_clear + 8 * q, clears >> q & 1)))) break;
+          clears ^= 1u << q;
+        }
+        // the parts in this buffer have been multiplied
+        if (j >= 2 && !(ok = __all_sync(all, wait(b_used + 8 * q, ((j >> 1) & 1) ^ 1)))) break;
+        tc_fence_after();
+        // (with d = 64 lanes 64 .. 127 take the tile behind b and are not read)
+        const uint64_t db = sdesc_add(db0, s * L::stage);
+        const uint32_t td = tm + 128 * q;
 #pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk) mma_ss(td + 16 * kk, sdesc_add(db, kk * 2048), eye, id_t, 0u);
-      mma_commit(b_t + 8 * (j & 1));
-      if (++s == L::stages) { s = 0; ph ^= 1; }
-      return true;
-    };
-    int j = 0, m = 0, sm = 0;  // step, accumulation, stage of the products
-    int bh = bh0, i = 0;
-    Piece<kT> pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
-    while (bh <= bh1 && pc.count == 0) {
-      if (++bh <= bh1) pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
+        for (int kk = 0; kk < kT / 16; ++kk) mma_ss(td + 16 * kk, sdesc_add(db, kk * 2048), eye, id_t, 0u);
+        mma_commit(b_t + 8 * q);
+        if (++s == L::stages) { s = 0; ph ^= 1; }
+      }
     }
-    bool more = bh <= bh1;
-    if (more) ok = issue_t(0, pc.size(0));
-    while (ok && more) {
-      const int place = i % kFlush;
-      const bool end = place == kFlush - 1 || i + 1 == pc.count;
-      // the step behind this one
-      if (++i == pc.count) {
-        i = 0;
-        do {
-          if (++bh <= bh1) pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
-        } while (bh <= bh1 && pc.count == 0);
-        more = bh <= bh1;
+  } else if (warp == 18) {
+    // the products with the parts
+    constexpr uint32_t id_s = idesc_bf16(128, D, 0, 1);
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+    const uint64_t dc0 = sdesc(sb + L::tile, L::half, 1024);
+    int j = 0, m = 0, s = 0, ph = 0;
+    for (int bh = bh0; ok && bh <= bh1; ++bh) {
+      const int count = uniform(get_piece<kT>(P, lens, part, bh, rev).count);
+      for (int i = 0; i < count; ++i, ++j) {
+        const int place = i % kFlush, q = j & 1;
+        if (place == 0 && m >= 2 &&
+            !(ok = __all_sync(all, wait(b_flush + 8 * (m & 1), ((m >> 1) & 1) ^ 1)))) break;
+        if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph) && wait(b_ready + 8 * q, (j >> 1) & 1)))) break;
+        tc_fence_after();
+        const uint32_t td = tm + 256 + 128 * (m & 1), tp = tm + 128 * q, first = place != 0 ? 1u : 0u;
+        const uint64_t dc = sdesc_add(dc0, s * L::stage);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)  // lo2
+          mma_ts(td, tp + 64 + kk * 8, sdesc_add(dc, kk * 2048), id_s, kk > 0 ? 1u : first);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)  // lo
+          mma_ts(td, tp + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_s, 1u);
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)  // hi
+          mma_ts(td, tp + kk * 16, sdesc_add(dc, kk * 2048), id_s, 1u);
+        mma_commit(b_used + 8 * q);
+        mma_commit(b_empty + 8 * s);
+        if (place == kFlush - 1 || i + 1 == count) {
+          mma_commit(b_acc + 8 * (m & 1));
+          ++m;
+        }
+        if (++s == L::stages) { s = 0; ph ^= 1; }
       }
-      // (a partial one is cleared by workers that may be waiting, at a piece's
-      // end, for the products of this step: those go first then)
-      const bool ahead = more && pc.size(i) == kT;
-      if (ahead && !(ok = issue_t(j + 1, kT))) break;
-      const int q = j & 1;
-      if (place == 0 && m >= 2 &&
-          !(ok = __all_sync(all, wait(b_flush + 8 * (m & 1), ((m >> 1) & 1) ^ 1)))) break;
-      if (!(ok = __all_sync(all, wait(b_ready + 8 * q, (j >> 1) & 1)))) break;
-      tc_fence_after();
-      const uint32_t td = tm + 256 + 128 * (m & 1), tp = tm + 128 * q, first = place != 0 ? 1u : 0u;
-      const uint64_t dc = sdesc_add(dc0, sm * L::stage);
-#pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk)  // lo2
-        mma_ts(td, tp + 64 + kk * 8, sdesc_add(dc, kk * 2048), id_s, kk > 0 ? 1u : first);
-#pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk)  // lo
-        mma_ts(td, tp + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_s, 1u);
-#pragma unroll
-      for (int kk = 0; kk < kT / 16; ++kk)  // hi
-        mma_ts(td, tp + kk * 16, sdesc_add(dc, kk * 2048), id_s, 1u);
-      mma_commit(b_empty + 8 * sm);
-      if (end) {
-        mma_commit(b_acc + 8 * (m & 1));
-        ++m;
-      }
-      if (++sm == L::stages) sm = 0;
-      if (more && !ahead && !(ok = issue_t(j + 1, pc.size(i)))) break;
-      ++j;
     }
   } else {
     const int quad = warp & 3, group = warp >> 3, h = warp >> 2 & 1;
@@ -487,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Outputs of a segment, chunk by chunk.  Groups of warps, each thread a row:
 // four warps turn X into P; eight (two threads a row) weight T into its parts
 // and carry the state, fp32 in registers, bf16 in shared memory as operand;
-// four scale Z and bring out the results, through the a tile and a TMA store.
+// four scale Z and bring out the results, through the c tile and a TMA store.
 // Then a loader and an issuer warp.
 //
 // Where the state of a piece's entering side stands: element (row, col) at
@@ -507,7 +502,7 @@ struct OutSmem {
   static constexpr uint32_t s_bytes = D * D * 2;
   static constexpr uint32_t off_eye = off_s + s_bytes;
   static constexpr uint32_t off_bar = off_eye + kEyeBytes;
-  static constexpr uint32_t off_wt = off_bar + 160;        // the tokens' weights in a chunk
+  static constexpr uint32_t off_wt = off_bar + 192;        // the tokens' weights in a chunk
   static constexpr uint32_t off_tab = off_wt + 512;        // 32 zeros, then decay^k, k < 128
   static constexpr uint32_t used = off_tab + 160 * 4 + 1024;
   // one CTA per SM: it takes all of tensor memory
@@ -526,22 +521,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = align1k(smem_raw);
   const uint32_t sb = smem_u32(base);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::off_bar);
-  const uint32_t b_full = smem_u32(bars);
-  const uint32_t b_ea = smem_u32(bars + 2);    // a tile's results stored
-  const uint32_t b_ebc = smem_u32(bars + 4);   // b and c read
-  const uint32_t b_x = smem_u32(bars + 6);     // X in TMEM
-  const uint32_t b_t = smem_u32(bars + 7);     // T in TMEM
-  const uint32_t b_z = smem_u32(bars + 8);     // Z in TMEM (the bf16 state read)
-  const uint32_t b_u = smem_u32(bars + 9);     // (w b)^T c in TMEM
-  const uint32_t b_o = smem_u32(bars + 10);    // O in TMEM
-  const uint32_t b_p = smem_u32(bars + 11);    // P in TMEM
-  const uint32_t b_zs = smem_u32(bars + 12);   // Z scaled
-  const uint32_t b_free = smem_u32(bars + 13); // O read
-  const uint32_t b_w = smem_u32(bars + 14);    // parts in TMEM
-  const uint32_t b_sr = smem_u32(bars + 15);   // bf16 state written
-  const uint32_t b_clear = smem_u32(bars + 16);  // rows behind the end cleared
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 17);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 18);
+  const uint32_t b_full = smem_u32(bars);      // [2] a and b there
+  const uint32_t b_fc = smem_u32(bars + 2);    // [2] c there
+  const uint32_t b_ea = smem_u32(bars + 4);    // [2] a read
+  const uint32_t b_eb = smem_u32(bars + 6);    // [2] b read
+  const uint32_t b_ec = smem_u32(bars + 8);    // [2] c read, and the results in its place stored
+  const uint32_t b_x = smem_u32(bars + 10);    // X in TMEM
+  const uint32_t b_t = smem_u32(bars + 11);    // T in TMEM
+  const uint32_t b_z = smem_u32(bars + 12);    // Z in TMEM (the bf16 state read)
+  const uint32_t b_u = smem_u32(bars + 13);    // state moved on
+  const uint32_t b_o = smem_u32(bars + 14);    // O in TMEM
+  const uint32_t b_p = smem_u32(bars + 15);    // P in TMEM
+  const uint32_t b_zs = smem_u32(bars + 16);   // Z scaled
+  const uint32_t b_free = smem_u32(bars + 17); // O read
+  const uint32_t b_w = smem_u32(bars + 18);    // parts in TMEM
+  const uint32_t b_sr = smem_u32(bars + 19);   // bf16 state written, accumulator scaled
+  const uint32_t b_clear = smem_u32(bars + 20);  // rows behind the end cleared
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
   float* pw = reinterpret_cast<float*>(base + L::off_tab);
   float* wt = reinterpret_cast<float*>(base + L::off_wt);
   const int tid = threadIdx.x, warp = tid / 32, quad = warp & 3;
@@ -550,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
   const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
   if (tid == 0) {
-    for (int x = 0; x < 11; ++x) mbar_init(smem_u32(bars + x), 1);
+    for (int x = 0; x < 15; ++x) mbar_init(smem_u32(bars + x), 1);
     mbar_init(b_p, 4);
     mbar_init(b_zs, 4);
     mbar_init(b_free, 4);
@@ -566,6 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  next_may_launch();
+  wait_for_previous();
   // X under P; Z under O; T, over 16 tokens' columns their hi (8) and lo (8)
   const uint32_t tX = *tslot, tO = tX + 128, tU = tX + 256, tT = tX + 384;
   const Waiter wait{status, abort_flag, limit};
@@ -581,13 +580,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
         for (int i = 0; i < pc.count; ++i, ++j) {
           const int s = j & 1;
+          // the tiles come free one by one: b behind T, a behind Z, c last; the
+          // next X needs a and b only
           const uint32_t st = sb + s * L::stage, bar = b_full + 8 * s, ph = ((j >> 1) & 1) ^ 1;
-          if (j >= 2 && !(ok = wait(b_ebc + 8 * s, ph))) break;
-          mbar_expect_tx(bar, L::stage);
+          if (j >= 2 && !(ok = wait(b_eb + 8 * s, ph))) break;
+          mbar_expect_tx(bar, 2 * L::tile);
           load_tile<D>(st + L::tile, &mb, pc.row(i), bh, bar, 16384);
-          load_tile<D>(st + 2 * L::tile, &mc, pc.row(i), bh, bar, 16384);
           if (j >= 2 && !(ok = wait(b_ea + 8 * s, ph))) break;
           if (!(withhold && j == 0 && part == 0)) load_tile<D>(st, &ma, pc.row(i), bh, bar, 16384);
+          if (j >= 2 && !(ok = wait(b_ec + 8 * s, ph))) break;
+          mbar_expect_tx(b_fc + 8 * s, L::tile);
+          load_tile<D>(st + 2 * L::tile, &mc, pc.row(i), bh, b_fc + 8 * s, 16384);
         }
       }
     }
@@ -622,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 8; ++kk) mma_ss(uT + 16 * kk, sdesc_add(dbt, kk * 2048), eye, id_t, 0u);
           mma_commit(b_t);
         }
+        mma_commit(b_eb + 8 * s);
         // Z = a S
         if (!(ok = __all_sync(all, wait(b_sr, j & 1)))) break;
         if (j > 0 && !(ok = __all_sync(all, wait(b_free, (j - 1) & 1)))) break;
@@ -630,12 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(uO, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_add(ds, kk * 2048), id_o, kk > 0);
         mma_commit(b_z);
-        // U = (w b)^T c
+        mma_commit(b_ea + 8 * s);
+        // S += (w b)^T c
+        if (!(ok = __all_sync(all, wait(b_fc + 8 * s, (j >> 1) & 1)))) break;
         if (!last) {
           if (!(ok = __all_sync(all, wait(b_w, ju & 1)))) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts(uU, uT + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_o, kk > 0);
+          for (int kk = 0; kk < 8; ++kk) mma_ts(uU, uT + kk * 16 + 8, sdesc_add(dc, kk * 2048), id_o, 1u);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) mma_ts(uU, uT + kk * 16, sdesc_add(dc, kk * 2048), id_o, 1u);
           mma_commit(b_u);
@@ -647,7 +653,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_ts(uO, uX + kk * 8, sdesc_add(dc, kk * 2048), id_o, 1u);
         mma_commit(b_o);
-        mma_commit(b_ebc + 8 * s);
       }
     }
   } else if (warp < 4) {
@@ -696,7 +701,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int CW = D / 2;
     const int col0 = h * CW;
     const bool mine = D == 128 || quad < 2;  // (d = 64: rows 64 .. 127 are not used)
-    float S[CW];
+    const uint32_t tS = tU + lane + col0, tW = tT + lane + 64 * h;
+    uint8_t* const sw = base + L::off_s;
+    // 32 values of the state (columns col0 + c ..): the bf16 copy of them, and
+    // scaled by f into the accumulator
+    auto put = [&](float* v, int c, float f, bool move) {
+#pragma unroll
+      for (int x = 0; x < 32; x += 8) {
+        const int u = (col0 + c + x) >> 3;
+        *reinterpret_cast<uint4*>(sw + (u >> 3) * (D * 128) + sw128(r, u & 7)) =
+            make_uint4(pack_bf16x2(v[x], v[x + 1]), pack_bf16x2(v[x + 2], v[x + 3]),
+                       pack_bf16x2(v[x + 4], v[x + 5]), pack_bf16x2(v[x + 6], v[x + 7]));
+      }
+      if (move) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] *= f;
+        tmem_st32(tS + c, v);
+      }
+    };
     int j = 0, ju = 0;
     for (int bh = bh0; bh <= bh1; ++bh) {
       const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
@@ -704,84 +726,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = bar_sync_and(2, 256, ok))) break;
       const int k = tid - 128;
       if (k < kC) wt[k] = R.w_sum * decay_power(l2, (REV ? k : kC - 1 - k) + R.e);
+      const float full = decay_power(l2, kC);
       asm volatile("bar.sync 2, 256;" ::: "memory");
-      if (mine && start.base && pc.count > 0) {
-        const float* p = start.base + start.stride * (start.by_piece ? pc.index : bh) + (r >> 2) * start.r4 + (r & 3) * start.r1;
-        if (start.c1 == 1) {
-#pragma unroll
-          for (int x = 0; x < CW; x += 4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(p + ((col0 + x) >> 2) * start.c4);
-            S[x] = f4.x; S[x + 1] = f4.y; S[x + 2] = f4.z; S[x + 3] = f4.w;
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < CW; ++x) S[x] = p[((col0 + x) >> 2) * start.c4 + (x & 3) * start.c1];
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < CW; ++x) S[x] = 0.f;
-      }
+      const float* p = start.base + start.stride * (start.by_piece ? pc.index : bh) + (r >> 2) * start.r4 + (r & 3) * start.r1;
       for (int i = 0; ok && i < pc.count; ++i, ++j) {
-        // the Z of the chunk before has read the last bf16 state
+        const bool last = i + 1 == pc.count;
+        const float fs = pc.size(i) == kC ? full : decay_power(l2, pc.size(i));
+        // the Z of the chunk before has read the last bf16 state, and the
+        // products of the chunk before have moved the accumulator
         if (j > 0 && !(ok = __all_sync(all, wait(b_z, (j - 1) & 1)))) break;
+        if (i > 0) {
+          if (!(ok = __all_sync(all, wait(b_u, (ju - 1) & 1)))) break;
+          tc_fence_after();
+        }
         if (mine) {
+          if (i > 0) {
+            float v[CW];
 #pragma unroll
-          for (int x = 0; x < CW; x += 8) {
-            const int u = (col0 + x) >> 3;
-            *reinterpret_cast<uint4*>(base + L::off_s + (u >> 3) * (D * 128) + sw128(r, u & 7)) =
-                make_uint4(pack_bf16x2(S[x], S[x + 1]), pack_bf16x2(S[x + 2], S[x + 3]),
-                           pack_bf16x2(S[x + 4], S[x + 5]), pack_bf16x2(S[x + 6], S[x + 7]));
+            for (int c = 0; c < CW; c += 32) tmem_ld32(tS + c, v + c);
+            tmem_wait_ld();
+            reg_fence<CW>(v);
+#pragma unroll
+            for (int c = 0; c < CW; c += 32) put(v + c, c, fs, !last);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < CW; c += 32) {
+              float v[32];
+              if (!start.base) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) v[x] = 0.f;
+              } else if (start.c1 == 1) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4) {
+                  const float4 f4 = *reinterpret_cast<const float4*>(p + ((col0 + c + x) >> 2) * start.c4);
+                  v[x] = f4.x; v[x + 1] = f4.y; v[x + 2] = f4.z; v[x + 3] = f4.w;
+                }
+              } else {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) v[x] = p[((col0 + c + x) >> 2) * start.c4 + (x & 3) * start.c1];
+              }
+              put(v, c, fs, !last);
+            }
           }
+          tmem_wait_st();
         }
         fence_async_smem();
+        tc_fence_before();
         __syncwarp();
         if (tid % 32 == 0) mbar_arrive(b_sr);
-        if (i + 1 == pc.count) continue;
+        if (last) continue;
         if (!(ok = __all_sync(all, wait(b_t, ju & 1)))) break;
         tc_fence_after();
         if (mine) {
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 16) {
-            float v[16];
-            uint32_t p[8];
-            const uint32_t t = tT + lane + 64 * h + c;
-            tmem_ld16(t, v);
-            float4 w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const float4*>(wt + 64 * h + c + 4 * x);
+          for (int c = 0; c < 64; c += 32) {
+            float v[32];
+            uint32_t q[8];
+            tmem_ld32(tW + c, v);
             tmem_wait_ld();
-            reg_fence<16>(v);
+            reg_fence<32>(v);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              v[4 * x] *= w[x].x; v[4 * x + 1] *= w[x].y;
-              v[4 * x + 2] *= w[x].z; v[4 * x + 3] *= w[x].w;
+            for (int x = 0; x < 8; ++x) {
+              const float4 w = *reinterpret_cast<const float4*>(wt + 64 * h + c + 4 * x);
+              v[4 * x] *= w.x; v[4 * x + 1] *= w.y; v[4 * x + 2] *= w.z; v[4 * x + 3] *= w.w;
             }
-            // the 16 columns read take hi and lo of their tokens
-            take_part(v, p);
-            tmem_st8u(t, p);
-            take_part(v, p);
-            tmem_st8u(t + 8, p);
+            // the columns of 16 tokens take their hi and lo parts
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              take_part(v + 16 * y, q);
+              tmem_st8u(tW + c + 16 * y, q);
+              take_part(v + 16 * y, q);
+              tmem_st8u(tW + c + 16 * y + 8, q);
+            }
           }
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
         if (tid % 32 == 0) mbar_arrive(b_w);
-        const float fs = decay_power(l2, pc.size(i));
-        if (!(ok = __all_sync(all, wait(b_u, ju & 1)))) break;
-        tc_fence_after();
-        if (mine) {
-#pragma unroll
-          for (int c = 0; c < CW; c += 16) {
-            float v[16];
-            tmem_ld16(tU + lane + col0 + c, v);
-            tmem_wait_ld();
-            reg_fence<16>(v);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) S[c + x] = fmaf(fs, S[c + x], v[x]);
-          }
-        }
-        tc_fence_before();
         ++ju;
       }
     }
@@ -795,12 +817,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < pc.count; ++i, ++j) {
         const int s = j & 1, nc = pc.size(i);
         const bool real = r < nc;
-        uint8_t* at = base + s * L::stage;
+        uint8_t* ct = base + s * L::stage + 2 * L::tile;
         float f = full;
         if (nc < kC) {
           if (REV) f = real ? R.w_st * decay_power(l2, nc - r - R.e) : 0.f;
-          if (ok && (ok = __all_sync(all, wait(b_full + 8 * s, (j >> 1) & 1)))) {
-            clear_rows<D, kC>(at + L::tile, at + 2 * L::tile, nc, r, 128);
+          if (ok && (ok = __all_sync(all, wait(b_full + 8 * s, (j >> 1) & 1) &&
+                                              wait(b_fc + 8 * s, (j >> 1) & 1)))) {
+            clear_rows<D, kC>(ct - L::tile, ct, nc, r, 128);
             fence_async_smem();
             __syncwarp();
             if (tid % 32 == 0) mbar_arrive(b_clear);
@@ -830,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && (ok = __all_sync(all, wait(b_o, j & 1)))) {
           tc_fence_after();
-          // all products that read this a tile are complete
+          // all products that read this c tile are complete
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -842,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (tid % 32 == 0) mbar_arrive(b_free);
             }
-            uint8_t* to = at + (c >> 6) * 16384;
+            uint8_t* to = ct + (c >> 6) * 16384;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               uint4 y = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
@@ -858,10 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r == 0) {
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_store_3d(&mo, sb + s * L::stage + h * 16384, h * 64, pc.row(i), bh);
+            tma_store_3d(&mo, sb + s * L::stage + 2 * L::tile + h * 16384, h * 64, pc.row(i), bh);
           tma_store_commit();
           tma_store_wait_read();
-          mbar_arrive(b_ea + 8 * s);
+          mbar_arrive(b_ec + 8 * s);
         }
       }
       if (!ok) break;
@@ -928,7 +951,7 @@ cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* 
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(P.parts, count), kThreads, smem, s>>>(m[0], m[1], m[2], m[3], log_decay, lens, jobs[0].sums,
+    kern<<<dim3(P.parts, count), kSumThreads, smem, s>>>(m[0], m[1], m[2], m[3], log_decay, lens, jobs[0].sums,
                                                       jobs[count - 1].sums, P, r[0], r[1], status, zero,
                                                       wait_limit(g), hold);
     return cudaGetLastError();
@@ -954,9 +977,8 @@ cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, con
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<P.parts, kThreads, smem, s>>>(ma, mb, mc, mo, log_decay, lens, v, static_cast<__nv_bfloat16*>(out),
-                                         P, R, status, zero, wait_limit(g), hold);
-    return cudaGetLastError();
+    return launch_behind(!zero, kern, dim3(P.parts), kThreads, smem, s, ma, mb, mc, mo, log_decay, lens, v,
+                         static_cast<__nv_bfloat16*>(out), P, R, status, zero, wait_limit(g), hold);
   };
   if (g.d == 128)
     return R.reverse ? go(decay_out_tc<128, true>, OutSmem<128>::total)

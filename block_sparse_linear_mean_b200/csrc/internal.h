@@ -299,13 +299,21 @@ cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, con
                                 const int32_t* lens, const DecayStart& start, void* out,
                                 const DecayParts& P, const DecayRole& R, const Geom& g, int32_t* status,
                                 int32_t* zero, cudaStream_t s);
-cudaError_t launch_decay_scan(float* sums, const float* first, float* final_state,
-                              const float* log_decay, const int32_t* lens, const DecayPlan& P,
-                              bool reverse, const Geom& g, cudaStream_t s);
-// the same over pieces, packed sums; `turned`: `first` is their transpose
-cudaError_t launch_decay_scan_parts(float* sums, const float* first, bool turned, float* final_state,
-                                    const float* log_decay, const int32_t* lens, const DecayParts& P,
-                                    bool reverse, const Geom& g, cudaStream_t s);
+// One set of sums -> states at the segments' entering sides, in place.
+struct DecayScanJob {
+  float* sums;
+  const float* first;  // state at the entering side of the sequence; null: zeros
+  float* last;         // state behind it (nullable)
+  bool turned;         // `first` is the transpose of the sums
+  bool reverse;
+};
+cudaError_t launch_decay_scan(const DecayScanJob& job, const float* log_decay, const int32_t* lens,
+                              const DecayPlan& P, const Geom& g, cudaStream_t s);
+// the same over pieces with packed sums, for one or two jobs; behind
+// launch_decay_sums_tc in the stream
+cudaError_t launch_decay_scan_parts(const DecayScanJob* jobs, int count, const float* log_decay,
+                                    const int32_t* lens, const DecayParts& P, const Geom& g,
+                                    cudaStream_t s);
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                               const int32_t* lens, const float* state_in, float* state_out, void* out,
                               const Geom& g, int32_t* zero, cudaStream_t s);

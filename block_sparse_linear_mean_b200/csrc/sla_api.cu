@@ -817,7 +817,8 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     if (!whole_heads(P) || state_out) {
       const sla::DecaySums job{k, v, sums, 1.0f, 0, false};
       SLA_CUDA(sla::launch_decay_sums_tc(&job, 1, log_decay, lens, P, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan_parts(sums, state_in, false, state_out, log_decay, lens, P, false, g, s));
+      const sla::DecayScanJob scan{sums, state_in, state_out, false, false};
+      SLA_CUDA(sla::launch_decay_scan_parts(&scan, 1, log_decay, lens, P, g, s));
       start = {sums, true};
       zero = nullptr;
     }
@@ -831,7 +832,7 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     return SLA_OK;
   }
   SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
-  SLA_CUDA(sla::launch_decay_scan(sums, state_in, state_out, log_decay, lens, P, false, g, s));
+  SLA_CUDA(sla::launch_decay_scan({sums, state_in, state_out, false, false}, log_decay, lens, P, g, s));
   SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, sums, int64_t(P.segs) * g.d * g.d, out,
                                       nullptr, P, R, g, nullptr, s));
   return SLA_OK;
@@ -883,12 +884,13 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
     sla::DecayRole Rs = Rq;
     if (need_r) {
       SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, P, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan_parts(rsums, dstate_out, false, dstate_in, log_decay, lens, P, true, g, s));
+      const sla::DecayScanJob scans[2] = {{rsums, dstate_out, dstate_in, false, true},
+                                          {sums, state_in, nullptr, true, false}};
+      SLA_CUDA(sla::launch_decay_scan_parts(scans, need_s ? 2 : 1, log_decay, lens, P, g, s));
       r_start = {rsums, true};
       zero = nullptr;
     }
     if (need_s) {
-      SLA_CUDA(sla::launch_decay_scan_parts(sums, state_in, true, nullptr, log_decay, lens, P, false, g, s));
       s_start = {sums, true};
       Rs.transposed = false;
     }
@@ -905,9 +907,9 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
   if (P.segs > 1) {
     float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
     SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
-    SLA_CUDA(sla::launch_decay_scan(sums, state_in, nullptr, log_decay, lens, P, false, g, s));
+    SLA_CUDA(sla::launch_decay_scan({sums, state_in, nullptr, false, false}, log_decay, lens, P, g, s));
     SLA_CUDA(sla::launch_decay_sums_simt(q, dout, log_decay, lens, rsums, P, 1, true, g.scale, g, nullptr, s));
-    SLA_CUDA(sla::launch_decay_scan(rsums, dstate_out, dstate_in, log_decay, lens, P, true, g, s));
+    SLA_CUDA(sla::launch_decay_scan({rsums, dstate_out, dstate_in, false, true}, log_decay, lens, P, g, s));
     s0 = sums;
     r0 = rsums;
     stride = P.segs * one;
