@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 64;
-constexpr int kRows = 4;  // rows in flight per thread
+constexpr int kWords = 32;  // 4-byte words in flight per thread
 
 // The side that is read and the side that is written, in elements.
 struct Side {
@@ -52,75 +52,64 @@ struct RotaryArgs {
   double turns[kMaxPairs];   // freq / 2 pi
 };
 
-// V consecutive elements of a row as fp32, in accesses of at most 16 bytes.
-template <int V>
-__device__ __forceinline__ void load_n(const float* p, float* x) {
-  if constexpr (V >= 4) {
+// V consecutive elements of a row, as the words they are stored in: rows in
+// flight cost registers by their bytes, not as fp32.
+template <typename T, int V>
+struct Words {
+  static constexpr int bytes = V * static_cast<int>(sizeof(T));
+  static constexpr int n = bytes < 4 ? 1 : bytes / 4;
+  uint32_t w[n];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (bytes >= 16) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p + i);
-      x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+      for (int i = 0; i < n; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + 4 * i);
+        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+      }
+    } else if constexpr (bytes == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x; w[1] = u.y;
+    } else if constexpr (bytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
-  } else if constexpr (V == 2) {
-    const float2 f = *reinterpret_cast<const float2*>(p);
-    x[0] = f.x; x[1] = f.y;
-  } else {
-    x[0] = *p;
   }
-}
-__device__ __forceinline__ void unpack2(uint32_t w, float* x) {
-  const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-  x[0] = f.x; x[1] = f.y;
-}
-template <int V>
-__device__ __forceinline__ void load_n(const __nv_bfloat16* p, float* x) {
-  if constexpr (V == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    unpack2(u.x, x); unpack2(u.y, x + 2); unpack2(u.z, x + 4); unpack2(u.w, x + 6);
-  } else if constexpr (V == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    unpack2(u.x, x); unpack2(u.y, x + 2);
-  } else if constexpr (V == 2) {
-    unpack2(*reinterpret_cast<const uint32_t*>(p), x);
-  } else {
-    x[0] = __bfloat162float(*p);
-  }
-}
-template <int V>
-__device__ __forceinline__ void store_n(float* p, const float* x) {
-  if constexpr (V >= 4) {
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (bytes >= 16) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  } else if constexpr (V == 2) {
-    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
-  } else {
-    *p = x[0];
+      for (int i = 0; i < n; i += 4)
+        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p) + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (bytes == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (bytes == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+    }
   }
-}
-__device__ __forceinline__ uint32_t pack2(const float* x) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <int V>
-__device__ __forceinline__ void store_n(__nv_bfloat16* p, const float* x) {
-  if constexpr (V == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x), pack2(x + 2), pack2(x + 4), pack2(x + 6));
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x), pack2(x + 2));
-  } else if constexpr (V == 2) {
-    *reinterpret_cast<uint32_t*>(p) = pack2(x);
-  } else {
-    *p = __float2bfloat16_rn(x[0]);
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
   }
-}
+  // elements i and i + 1 (i even), or the only one
+  __device__ __forceinline__ void put(int i, float a, float b) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(a);
+      if constexpr (V > 1) w[i + 1] = __float_as_uint(b);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+};
 
 // A unit is V pairs of one token's row (2 V channels); the d / (2 V) units of
 // a row take one thread each.  The first pairs / V of them turn, the rest are
 // copied.  Half layout: channels [a, a + V) and [a + pairs, + V); interleaved:
 // 2 V neighbours.
 template <typename TIn, typename TOut, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs A) {
   __shared__ double turns[kMaxPairs];
   if (threadIdx.x < kMaxPairs) turns[threadIdx.x] = A.turns[threadIdx.x];
   __syncthreads();
@@ -187,43 +176,49 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const i64 in0 = b * A.in.b + n_in * A.in.n, out0 = b * A.out.b + n_out * A.out.n;
   const int row0 = blockIdx.y * A.rows_per_group;
   const int row1 = min(row0 + A.rows_per_group, A.tensors * A.H);
+  // INTER: one access of 2 V; half: one of V for each piece
+  constexpr int VA = INTER ? 2 * V : V;
+  using In = Words<TIn, VA>;
+  using Out = Words<TOut, VA>;
+  constexpr int per_row = In::n * (INTER ? 1 : 2);
+  constexpr int kRows = kWords / per_row < 8 ? kWords / per_row : 8;
   for (int r0 = row0; r0 < row1; r0 += kRows) {
-    float x[kRows][2 * V];
+    In x[kRows][INTER ? 1 : 2];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       const int r = r0 + k;
       if (r < row1) {
         const int second = r >= A.H, h = second ? r - A.H : r;
         const TIn* src = static_cast<const TIn*>(second ? A.src[1] : A.src[0]) + in0 + h * A.in.h;
-        if (INTER) {
-          load_n<2 * V>(src + c0, x[k]);
-        } else {
-          load_n<V>(src + c0, x[k]);
-          load_n<V>(src + c1, x[k] + V);
-        }
+        x[k][0].load(src + c0);
+        if constexpr (!INTER) x[k][1].load(src + c1);
       }
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       const int r = r0 + k;
       if (r < row1) {
-        if (turn) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float& a = INTER ? x[k][2 * i] : x[k][i];
-            float& c = INTER ? x[k][2 * i + 1] : x[k][V + i];
-            const float ya = a * cs[i] - c * sn[i], yc = c * cs[i] + a * sn[i];
-            a = ya;
-            c = yc;
-          }
-        }
         const int second = r >= A.H, h = second ? r - A.H : r;
         TOut* dst = static_cast<TOut*>(second ? A.dst[1] : A.dst[0]) + out0 + h * A.out.h;
-        if (INTER) {
-          store_n<2 * V>(dst + c0, x[k]);
+        if constexpr (INTER) {
+          Out y;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float a = x[k][0].get(2 * i), b = x[k][0].get(2 * i + 1);
+            y.put(2 * i, turn ? a * cs[i] - b * sn[i] : a, turn ? b * cs[i] + a * sn[i] : b);
+          }
+          y.store(dst + c0);
         } else {
-          store_n<V>(dst + c0, x[k]);
-          store_n<V>(dst + c1, x[k] + V);
+          Out y, z;
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const int j = V > 1 ? i + 1 : i;
+            const float a0 = x[k][0].get(i), b0 = x[k][1].get(i), a1 = x[k][0].get(j), b1 = x[k][1].get(j);
+            y.put(i, turn ? a0 * cs[i] - b0 * sn[i] : a0, turn ? a1 * cs[j] - b1 * sn[j] : a1);
+            z.put(i, turn ? b0 * cs[i] + a0 * sn[i] : b0, turn ? b1 * cs[j] + a1 * sn[j] : b1);
+          }
+          y.store(dst + c0);
+          z.store(dst + c1);
         }
       }
     }

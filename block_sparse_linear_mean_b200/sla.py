@@ -556,30 +556,33 @@ _DTYPES = {torch.float32: SLA_F32, torch.bfloat16: SLA_BF16}
 _TORCH_DTYPES = {SLA_F32: torch.float32, SLA_BF16: torch.bfloat16}
 
 
-def _enqueue(name, fn, p, args, device):
-    """Calls ``fn(p, *args, stream)`` on ``device``'s current stream."""
-    if device.index == torch.cuda.current_device():
-        st = fn(ctypes.byref(p), *args, torch.cuda.current_stream().cuda_stream)
+def _enqueue(name, fn, p, args, device: int):
+    """Calls ``fn(p, *args, stream)`` on the current stream of device number
+    ``device``.  (The calls below cost the host more than their kernels cost
+    the GPU at a few tokens, so the checks and this are kept short: integers
+    for devices, the raw stream.)"""
+    if device == torch._C._cuda_getDevice():
+        st = fn(ctypes.byref(p), *args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(ctypes.byref(p), *args, torch.cuda.current_stream().cuda_stream)
+            st = fn(ctypes.byref(p), *args, torch._C._cuda_getCurrentRawStream(device))
     if st != SLA_OK:
         raise SlaError(name, st)
 
 
-def _want(t: torch.Tensor, name: str, shape, dtype, device, dense=True):
+def _want(t: torch.Tensor, name: str, shape, dtype, device: int, dense=True):
     """Refuses a tensor that is not what the call is about to read."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: want {dtype} {list(shape)} on {device}, got {t.dtype} "
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise ValueError(f"{name}: want {dtype} {list(shape)} on cuda:{device}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous tensor, got strides {t.stride()}")
 
 
-def _cuda(t: torch.Tensor, name: str) -> torch.device:
+def _cuda(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name}: want a CUDA tensor, got one on {t.device}")
-    return t.device
+    return t.get_device()
 
 
 def rotary(rot_dim: int, layout: str = "half", axis_pairs=None, grid=None, origin=(0, 0, 0),
@@ -616,9 +619,9 @@ def _index(p, t, axes, device, name):
     (the axes dim may be left out with one axis)."""
     if t is None:
         return None, 0
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: want contiguous int32 on {device}")
-    shape = tuple(t.shape)
+    if t.dtype is not torch.int32 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous int32 on cuda:{device}")
+    shape = t.shape
     if shape == (axes, p.N) or (axes == 1 and shape == (p.N,)):
         return t.data_ptr(), 0
     if shape == (p.B, axes, p.N) or (axes == 1 and shape == (p.B, p.N)):
@@ -626,27 +629,37 @@ def _index(p, t, axes, device, name):
     raise ValueError(f"{name}: want [{axes}, {p.N}] or [{p.B}, {axes}, {p.N}], got {list(shape)}")
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _rotary_call(p, r, raw, rot, positions, perm, inverse):
-    dev = _cuda(raw[0], "q")
+    x, z = raw[0], rot[0]
+    dev = _cuda(x, "q")
     shape = (p.B, p.H, p.N, p.d)
+    dtype = _TORCH_DTYPES[p.dtype]
     if len(raw) != len(rot) or not 1 <= len(raw) <= 2:
         raise ValueError("one or two tensors on both sides")
-    strides = raw[0].stride()
-    for x, y in zip(raw, rot):
-        _want(x, "raw side", shape, _TORCH_DTYPES[p.dtype], dev, dense=False)
-        _want(y, "turned side", shape, rot[0].dtype, dev)
-        if x.stride(3) != 1 or any(a != b for n, a, b in zip(shape, x.stride(), strides) if n > 1):
-            raise ValueError("raw side: want both tensors with the same strides, channels adjacent")
-    if rot[0].dtype not in _DTYPES:
-        raise ValueError(f"turned side: {rot[0].dtype} is not supported")
+    _want(x, "raw side", shape, dtype, dev, dense=False)
+    _want(z, "turned side", shape, z.dtype, dev)
+    strides = x.stride()
+    if len(raw) == 2:
+        _want(raw[1], "raw side", shape, dtype, dev, dense=False)
+        _want(rot[1], "turned side", shape, z.dtype, dev)
+        other = raw[1].stride()
+        if other != strides and any(a != b for n, a, b in zip(shape, other, strides) if n > 1):
+            raise ValueError("raw side: want both tensors with the same strides")
+    if strides[3] != 1:
+        raise ValueError("raw side: want adjacent channels")
+    if z.dtype not in _DTYPES:
+        raise ValueError(f"turned side: {z.dtype} is not supported")
     pos, batched = _index(p, positions, r.axes, dev, "positions")
     if perm is not None:
         _want(perm, "perm", (p.N,), torch.int32, dev)
-    args = (ctypes.byref(r), (ctypes.c_int64 * 3)(*strides[:3]), raw[0].data_ptr(),
-            raw[1].data_ptr() if len(raw) > 1 else None, rot[0].data_ptr(),
-            rot[1].data_ptr() if len(rot) > 1 else None, _DTYPES[rot[0].dtype], pos, batched,
-            _ptr(perm), 1 if inverse else 0)
-    _enqueue("sla_apply_rotary", lib().sla_apply_rotary, p, args, dev)
+    _enqueue("sla_apply_rotary", lib().sla_apply_rotary, p,
+             (ctypes.byref(r), _Strides(*strides[:3]), x.data_ptr(),
+              raw[1].data_ptr() if len(raw) > 1 else None, z.data_ptr(),
+              rot[1].data_ptr() if len(rot) > 1 else None, _DTYPES[z.dtype], pos, batched,
+              _ptr(perm), 1 if inverse else 0), dev)
 
 
 def apply_rotary(p: sla_params, r: sla_rotary, q: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -660,7 +673,7 @@ def apply_rotary(p: sla_params, r: sla_rotary, q: torch.Tensor, k: Optional[torc
     order is given; fp32 is allowed for bf16 inputs)."""
     raw = (q,) if k is None else (q, k)
     if out is None:
-        rot = tuple(torch.empty(p.B, p.H, p.N, p.d, dtype=q.dtype, device=q.device) for _ in raw)
+        rot = tuple([torch.empty_like(x, memory_format=torch.contiguous_format) for x in raw])
     else:
         rot = (out,) if torch.is_tensor(out) else tuple(out)
     _rotary_call(p, r, raw, rot, positions, perm, False)
@@ -695,8 +708,8 @@ def _decay_inputs(p, tokens, log_decay, lens, states, ws=None):
     for name, t in states:
         if t is not None:
             _want(t, name, (p.B, p.H, p.d, p.d), torch.float32, dev)
-    if ws is not None and (ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous()):
-        raise ValueError(f"ws: want contiguous uint8 on {dev} (sla.workspace)")
+    if ws is not None and (ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws: want contiguous uint8 on cuda:{dev} (sla.workspace)")
     return dev
 
 
@@ -715,9 +728,9 @@ def decay_attention(p: sla_params, q, k, v, log_decay: torch.Tensor,
     else:
         _want(out, "out", q.shape, q.dtype, dev)
     if state_out is None:
-        state_out = torch.empty(p.B, p.H, p.d, p.d, dtype=torch.float32, device=dev)
+        state_out = torch.empty((p.B, p.H, p.d, p.d), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = workspace(p, SLA_OP_DECAY, dev)
+        ws = workspace(p, SLA_OP_DECAY, q.device)
     _enqueue("sla_decay_attention", lib().sla_decay_attention, p,
              (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lens), _ptr(state),
               out.data_ptr(), state_out.data_ptr(), ws.data_ptr(), ws.numel()), dev)
@@ -734,9 +747,9 @@ def decay_attention_backward(p: sla_params, q, k, v, log_decay: torch.Tensor, do
     dev = _decay_inputs(p, (("q", q), ("k", k), ("v", v), ("dout", dout)), log_decay, lens,
                         (("state", state), ("dstate", dstate)), ws)
     dq, dk, dv = (torch.empty_like(q) for _ in range(3))
-    ds = torch.empty(p.B, p.H, p.d, p.d, dtype=torch.float32, device=dev)
+    ds = torch.empty((p.B, p.H, p.d, p.d), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = workspace(p, SLA_OP_DECAY_BACKWARD, dev)
+        ws = workspace(p, SLA_OP_DECAY_BACKWARD, q.device)
     _enqueue("sla_decay_attention_backward", lib().sla_decay_attention_backward, p,
              (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lens), _ptr(state),
               dout.data_ptr(), _ptr(dstate), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
