@@ -259,10 +259,8 @@ struct UniformSegments {
 struct PieceSegments {
   DecayParts P;
   static constexpr bool packed = true;
-  // the part that holds chunk g: the last k with total k / parts <= g
-  __device__ int part(i64 g) const { return static_cast<int>(((g + 1) * P.parts - 1) / P.total); }
-  __device__ int first(int bh) const { return part(i64(bh) * P.chunks); }
-  __device__ int count(int bh) const { return part(i64(bh + 1) * P.chunks - 1) - first(bh) + 1; }
+  __device__ int first(int bh) const { return P.part(i64(bh) * P.chunks); }
+  __device__ int count(int bh) const { return P.part(i64(bh + 1) * P.chunks - 1) - first(bh) + 1; }
   // first token of part k within head bh
   __device__ int begin(int bh, int k) const {
     return static_cast<int>(min(max(P.begin(k) - i64(bh) * P.chunks, i64(0)), i64(P.chunks))) * 128;

@@ -489,9 +489,32 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 // base + (row / 4) * r4 + (row % 4) * r1 + (col / 4) * c4 + (col % 4) * c1.
 struct StateView {
   const float* base;
-  i64 stride;          // of the piece's place, or of the head
+  i64 stride;          // of the place in the sums' workspace, or of the head
   int by_piece;
   int r4, r1, c4, c1;
+};
+
+// One launch does one role (the forward) or three (the gradients): CTA x takes
+// part x / jobs in role x % jobs, so that dk and dv, which read the same four
+// tensors, walk over them side by side and the second finds them in L2.
+struct OutJob {
+  int a, b, c, o;      // tensor maps
+  __nv_bfloat16* out;
+  StateView start;
+  DecayRole R;
+};
+struct OutArgs {
+  CUtensorMap maps[7];
+  OutJob job[3];
+  int jobs;
+  DecayParts P;        // of this launch
+  DecayParts sums;     // of the sums: every cut of P is one of theirs
+  const float* log_decay;
+  const int32_t* lens;
+  int32_t* status;
+  int32_t* zero;
+  long long limit;
+  int withhold;
 };
 
 template <int D>
@@ -509,13 +532,8 @@ struct OutSmem {
   static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;
 };
 
-template <int D, bool REV>
-__global__ void __launch_bounds__(kThreads, 1)
-    decay_out_tc(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                 const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap mo,
-                 const float* __restrict__ log_decay, const int32_t* __restrict__ lens,
-                 StateView start, __nv_bfloat16* __restrict__ out, DecayParts P, DecayRole R,
-                 int32_t* status, int32_t* zero, long long limit, int withhold) {
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constant__ OutArgs A) {
   using L = OutSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1k(smem_raw);
@@ -542,8 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* pw = reinterpret_cast<float*>(base + L::off_tab);
   float* wt = reinterpret_cast<float*>(base + L::off_wt);
   const int tid = threadIdx.x, warp = tid / 32, quad = warp & 3;
-  const int part = blockIdx.x;
-  if (zero && tid == 0 && part == 0) *zero = 0;
+  const int part = blockIdx.x / A.jobs;
+  const OutJob& J = A.job[blockIdx.x % A.jobs];
+  const DecayParts& P = A.P;
+  const DecayRole R = J.R;
+  const bool rev = R.reverse;
+  const float* const log_decay = A.log_decay;
+  const int32_t* const lens = A.lens;
+  if (A.zero && tid == 0 && blockIdx.x == 0) *A.zero = 0;
   const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
   const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
   if (tid == 0) {
@@ -567,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_previous();
   // X under P; Z under O; T, over 16 tokens' columns their hi (8) and lo (8)
   const uint32_t tX = *tslot, tO = tX + 128, tU = tX + 256, tT = tX + 384;
-  const Waiter wait{status, abort_flag, limit};
+  const Waiter wait{A.status, abort_flag, A.limit};
   const unsigned all = 0xffffffffu;
   const uint32_t lane = static_cast<uint32_t>(quad * 32) << 16;
   const int r = tid & 127;
@@ -575,9 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 16) {
     if (tid % 32 == 0) {
+      const CUtensorMap *ma = &A.maps[J.a], *mb = &A.maps[J.b], *mc = &A.maps[J.c];
       int j = 0;
       for (int bh = bh0; ok && bh <= bh1; ++bh) {
-        const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+        const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, rev);
         for (int i = 0; i < pc.count; ++i, ++j) {
           const int s = j & 1;
           // the tiles come free one by one: b behind T, a behind Z, c last; the
@@ -585,12 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t st = sb + s * L::stage, bar = b_full + 8 * s, ph = ((j >> 1) & 1) ^ 1;
           if (j >= 2 && !(ok = wait(b_eb + 8 * s, ph))) break;
           mbar_expect_tx(bar, 2 * L::tile);
-          load_tile<D>(st + L::tile, &mb, pc.row(i), bh, bar, 16384);
+          load_tile<D>(st + L::tile, mb, pc.row(i), bh, bar, 16384);
           if (j >= 2 && !(ok = wait(b_ea + 8 * s, ph))) break;
-          if (!(withhold && j == 0 && part == 0)) load_tile<D>(st, &ma, pc.row(i), bh, bar, 16384);
+          if (!(A.withhold && j == 0 && blockIdx.x == 0)) load_tile<D>(st, ma, pc.row(i), bh, bar, 16384);
           if (j >= 2 && !(ok = wait(b_ec + 8 * s, ph))) break;
           mbar_expect_tx(b_fc + 8 * s, L::tile);
-          load_tile<D>(st + 2 * L::tile, &mc, pc.row(i), bh, b_fc + 8 * s, 16384);
+          load_tile<D>(st + 2 * L::tile, mc, pc.row(i), bh, b_fc + 8 * s, 16384);
         }
       }
     }
@@ -603,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    da0 = sdesc(sb, 16, 1024), dt0 = sdesc(sb, 16384, 1024);
     int j = 0, ju = 0, clears = 0;  // chunk; chunk that moves the state; partial chunk
     for (int bh = bh0; ok && bh <= bh1; ++bh) {
-      const Piece<kC> pc = uniform(get_piece<kC>(P, lens, part, bh, REV));
+      const Piece<kC> pc = uniform(get_piece<kC>(P, lens, part, bh, rev));
       for (int i = 0; i < pc.count; ++i, ++j) {
         const int s = j & 1;
         const bool last = i + 1 == pc.count;
@@ -659,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ P
     int j = 0;
     for (int bh = bh0; bh <= bh1; ++bh) {
-      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, rev);
       // (every warp comes here, also one whose wait gave up)
       if (!(ok = bar_sync_and(1, 128, ok))) break;
       pw[32 + r] = R.w_in * decay_power(decay_log2(log_decay[bh % P.H]), r);
@@ -673,19 +698,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
           uint32_t pk[16];
-          if (REV ? cb < quad : cb > quad) {
+          if (rev ? cb < quad : cb > quad) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0u;
           } else {
             float v[32];
             tmem_ld32(tX + lane + cb * 32, v);
-            const float* w = pw + 32 + (REV ? cb * 32 - r : r - cb * 32);
+            const float* w = pw + 32 + (rev ? cb * 32 - r : r - cb * 32);
             tmem_wait_ld();
             reg_fence<32>(v);
+            if (rev) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              pk[x] = REV ? pack_bf16x2(v[2 * x] * w[2 * x], v[2 * x + 1] * w[2 * x + 1])
-                          : pack_bf16x2(v[2 * x] * w[-2 * x], v[2 * x + 1] * w[-2 * x - 1]);
+              for (int x = 0; x < 32; ++x) v[x] *= w[x];
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] *= w[-x];
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) pk[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
           }
           tmem_st16u(tX + lane + cb * 16, pk);
         }
@@ -701,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int CW = D / 2;
     const int col0 = h * CW;
     const bool mine = D == 128 || quad < 2;  // (d = 64: rows 64 .. 127 are not used)
+    const StateView& start = J.start;
     const uint32_t tS = tU + lane + col0, tW = tT + lane + 64 * h;
     uint8_t* const sw = base + L::off_s;
     // 32 values of the state (columns col0 + c ..): the bf16 copy of them, and
@@ -721,14 +752,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int j = 0, ju = 0;
     for (int bh = bh0; bh <= bh1; ++bh) {
-      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, rev);
       const double l2 = decay_log2(log_decay[bh % P.H]);
       if (!(ok = bar_sync_and(2, 256, ok))) break;
       const int k = tid - 128;
-      if (k < kC) wt[k] = R.w_sum * decay_power(l2, (REV ? k : kC - 1 - k) + R.e);
+      if (k < kC) wt[k] = R.w_sum * decay_power(l2, (rev ? k : kC - 1 - k) + R.e);
       const float full = decay_power(l2, kC);
       asm volatile("bar.sync 2, 256;" ::: "memory");
-      const float* p = start.base + start.stride * (start.by_piece ? pc.index : bh) + (r >> 2) * start.r4 + (r & 3) * start.r1;
+      // the sums' piece at this one's entering side
+      const i64 enter = i64(bh) * P.chunks + (rev ? (pc.t0 + pc.cap - 1) / kC : pc.t0 / kC);
+      const float* p = start.base + start.stride * (start.by_piece ? A.sums.part(enter) + bh : bh) +
+                       (r >> 2) * start.r4 + (r & 3) * start.r1;
       for (int i = 0; ok && i < pc.count; ++i, ++j) {
         const bool last = i + 1 == pc.count;
         const float fs = pc.size(i) == kC ? full : decay_power(l2, pc.size(i));
@@ -811,16 +845,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ results
     int j = 0;
     for (int bh = bh0; bh <= bh1; ++bh) {
-      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, REV);
+      const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, rev);
       const double l2 = decay_log2(log_decay[bh % P.H]);
-      const float full = R.w_st * decay_power(l2, (REV ? kC - 1 - r : r) + 1 - R.e);
+      const float full = R.w_st * decay_power(l2, (rev ? kC - 1 - r : r) + 1 - R.e);
       for (int i = 0; i < pc.count; ++i, ++j) {
         const int s = j & 1, nc = pc.size(i);
         const bool real = r < nc;
         uint8_t* ct = base + s * L::stage + 2 * L::tile;
         float f = full;
         if (nc < kC) {
-          if (REV) f = real ? R.w_st * decay_power(l2, nc - r - R.e) : 0.f;
+          if (rev) f = real ? R.w_st * decay_power(l2, nc - r - R.e) : 0.f;
           if (ok && (ok = __all_sync(all, wait(b_full + 8 * s, (j >> 1) & 1) &&
                                               wait(b_fc + 8 * s, (j >> 1) & 1)))) {
             clear_rows<D, kC>(ct - L::tile, ct, nc, r, 128);
@@ -881,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r == 0) {
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_store_3d(&mo, sb + s * L::stage + 2 * L::tile + h * 16384, h * 64, pc.row(i), bh);
+            tma_store_3d(&A.maps[J.o], sb + s * L::stage + 2 * L::tile + h * 16384, h * 64, pc.row(i), bh);
           tma_store_commit();
           tma_store_wait_read();
           mbar_arrive(b_ec + 8 * s);
@@ -890,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // whole chunks behind the sequence's end
       for (int t = pc.count * kC + r; t < pc.cap; t += kC) {
-        uint4* dst = reinterpret_cast<uint4*>(out + (i64(bh) * P.N + pc.t0 + t) * D);
+        uint4* dst = reinterpret_cast<uint4*>(J.out + (i64(bh) * P.N + pc.t0 + t) * D);
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) dst[x] = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -927,13 +961,14 @@ bool decay_tc_supported(const Geom& g) {
   return g.dtype == SLA_BF16 && !(g.flags & SLA_FLAG_SIMT);
 }
 
-DecayParts decay_parts(const Geom& g) {
+DecayParts decay_parts(const Geom& g, int jobs, bool sums) {
   DecayParts P;
   P.N = g.N;
   P.H = g.H;
   P.chunks = (g.N + kC - 1) / kC;
   P.total = i64(P.chunks) * g.BH;
-  P.parts = static_cast<int>(std::min<i64>(P.total, 148));
+  P.parts = static_cast<int>(std::min<i64>(P.total, 148 / jobs));
+  if (sums && i64(P.parts) * jobs <= P.total) P.parts *= jobs;
   return P;
 }
 
@@ -959,32 +994,40 @@ cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* 
   return g.d == 128 ? go(decay_sums_tc<128>, SumsSmem<128>::total) : go(decay_sums_tc<64>, SumsSmem<64>::total);
 }
 
-cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, const float* log_decay,
-                                const int32_t* lens, const DecayStart& start, void* out,
-                                const DecayParts& P, const DecayRole& R, const Geom& g, int32_t* status,
-                                int32_t* zero, cudaStream_t s) {
-  CUtensorMap ma, mb, mc, mo;
-  if (!token_map(&ma, a, g, kC) || !token_map(&mb, b, g, kC) || !token_map(&mc, c, g, kC) ||
-      !token_map(&mo, out, g, kC))
-    return cudaErrorInvalidValue;
-  const int hold = debug_withhold(g, SLA_WITHHOLD_ATTENTION) ? 1 : 0;
+cudaError_t launch_decay_out_tc(const void* const* tensors, int count, const DecayOut* jobs, int njobs,
+                                const float* log_decay, const int32_t* lens, const DecayParts& P,
+                                const DecayParts& sums, const Geom& g, int32_t* status, int32_t* zero,
+                                cudaStream_t s) {
+  OutArgs A{};
+  if (count > 7 || njobs > 3) return cudaErrorInvalidValue;
+  for (int i = 0; i < count; ++i)
+    if (!token_map(&A.maps[i], tensors[i], g, kC)) return cudaErrorInvalidValue;
   const int d = g.d;
-  StateView v{start.state, i64(d) * d, start.packed, 0, 0, 0, 0};
-  if (start.packed && !R.transposed) v.r4 = 16, v.r1 = 4, v.c4 = 4 * d, v.c1 = 1;
-  if (start.packed && R.transposed) v.r4 = 4 * d, v.r1 = 1, v.c4 = 16, v.c1 = 4;
-  if (!start.packed && !R.transposed) v.r4 = 4 * d, v.r1 = d, v.c4 = 4, v.c1 = 1;
-  if (!start.packed && R.transposed) v.r4 = 4, v.r1 = 1, v.c4 = 4 * d, v.c1 = d;
+  for (int i = 0; i < njobs; ++i) {
+    const DecayOut& j = jobs[i];
+    StateView v{j.start.state, i64(d) * d, j.start.packed, 0, 0, 0, 0};
+    if (j.start.packed && !j.role.transposed) v.r4 = 16, v.r1 = 4, v.c4 = 4 * d, v.c1 = 1;
+    if (j.start.packed && j.role.transposed) v.r4 = 4 * d, v.r1 = 1, v.c4 = 16, v.c1 = 4;
+    if (!j.start.packed && !j.role.transposed) v.r4 = 4 * d, v.r1 = d, v.c4 = 4, v.c1 = 1;
+    if (!j.start.packed && j.role.transposed) v.r4 = 4, v.r1 = 1, v.c4 = 4 * d, v.c1 = d;
+    A.job[i] = OutJob{j.a, j.b, j.c, j.out, static_cast<__nv_bfloat16*>(const_cast<void*>(tensors[j.out])),
+                      v, j.role};
+  }
+  A.jobs = njobs;
+  A.P = P;
+  A.sums = sums;
+  A.log_decay = log_decay;
+  A.lens = lens;
+  A.status = status;
+  A.zero = zero;
+  A.limit = wait_limit(g);
+  A.withhold = debug_withhold(g, SLA_WITHHOLD_ATTENTION) ? 1 : 0;
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    return launch_behind(!zero, kern, dim3(P.parts), kThreads, smem, s, ma, mb, mc, mo, log_decay, lens, v,
-                         static_cast<__nv_bfloat16*>(out), P, R, status, zero, wait_limit(g), hold);
+    return launch_behind(!zero, kern, dim3(P.parts * njobs), kThreads, smem, s, A);
   };
-  if (g.d == 128)
-    return R.reverse ? go(decay_out_tc<128, true>, OutSmem<128>::total)
-                     : go(decay_out_tc<128, false>, OutSmem<128>::total);
-  return R.reverse ? go(decay_out_tc<64, true>, OutSmem<64>::total)
-                   : go(decay_out_tc<64, false>, OutSmem<64>::total);
+  return g.d == 128 ? go(decay_out_tc<128>, OutSmem<128>::total) : go(decay_out_tc<64>, OutSmem<64>::total);
 }
 
 }  // namespace sla

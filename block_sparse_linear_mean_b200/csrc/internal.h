@@ -276,8 +276,15 @@ struct DecayParts {
   __host__ __device__
 #endif
   i64 begin(int k) const { return total * k / parts; }
+  // the part that holds chunk g: the last k with begin(k) <= g
+#ifdef __CUDACC__
+  __host__ __device__
+#endif
+  int part(i64 g) const { return static_cast<int>(((g + 1) * parts - 1) / total); }
 };
-DecayParts decay_parts(const Geom& g);
+// Parts of a launch of the output kernel with `jobs` roles, or of the sums
+// that go with it (finer where there are chunks enough, cuts at the same places).
+DecayParts decay_parts(const Geom& g, int jobs, bool sums);
 struct DecaySums {
   const void *b, *c;
   float* sums;
@@ -295,10 +302,15 @@ struct DecayStart {
   const float* state;
   bool packed;
 };
-cudaError_t launch_decay_out_tc(const void* a, const void* b, const void* c, const float* log_decay,
-                                const int32_t* lens, const DecayStart& start, void* out,
-                                const DecayParts& P, const DecayRole& R, const Geom& g, int32_t* status,
-                                int32_t* zero, cudaStream_t s);
+struct DecayOut {
+  int a, b, c, out;   // of the launch's tensors
+  DecayStart start;
+  DecayRole role;
+};
+cudaError_t launch_decay_out_tc(const void* const* tensors, int count, const DecayOut* jobs, int njobs,
+                                const float* log_decay, const int32_t* lens, const DecayParts& P,
+                                const DecayParts& sums, const Geom& g, int32_t* status, int32_t* zero,
+                                cudaStream_t s);
 // One set of sums -> states at the segments' entering sides, in place.
 struct DecayScanJob {
   float* sums;

@@ -190,7 +190,7 @@ sla::DecayPlan decay_plan(const Geom& g) {
 DecayWs decay_ws(const Geom& g, bool backward) {
   size_t states;  // in the workspace of one set of sums
   if (sla::decay_tc_supported(g)) {
-    states = size_t(sla::decay_parts(g).parts) + g.BH;
+    states = size_t(sla::decay_parts(g, backward ? 3 : 1, true).parts) + g.BH;
   } else {
     const sla::DecayPlan P = decay_plan(g);
     states = P.segs > 1 ? size_t(g.BH) * P.segs : 0;
@@ -811,7 +811,7 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     // the state that is handed on, to the next piece of a head or to the
     // caller, comes from the sums kernel, which keeps it to fp32 accuracy;
     // whole heads and no state wanted need no sums
-    const sla::DecayParts P = sla::decay_parts(g);
+    const sla::DecayParts P = sla::decay_parts(g, 1, false);
     sla::DecayStart start{state_in, false};
     int32_t* zero = status;
     if (!whole_heads(P) || state_out) {
@@ -822,7 +822,9 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
       start = {sums, true};
       zero = nullptr;
     }
-    SLA_CUDA(sla::launch_decay_out_tc(q, k, v, log_decay, lens, start, out, P, R, g, status, zero, s));
+    const void* tensors[] = {q, k, v, out};
+    const sla::DecayOut job{0, 1, 2, 3, start, R};
+    SLA_CUDA(sla::launch_decay_out_tc(tensors, 4, &job, 1, log_decay, lens, P, P, g, status, zero, s));
     return SLA_OK;
   }
   const sla::DecayPlan P = decay_plan(g);
@@ -874,7 +876,7 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
   const sla::DecayRole Rv{g.scale, 1.0f, g.scale, 1, true, false};
   const sla::DecayRole Rk{g.scale, 1.0f, g.scale, 1, true, true};
   if (sla::decay_tc_supported(g)) {
-    const sla::DecayParts P = sla::decay_parts(g);
+    const sla::DecayParts P = sla::decay_parts(g, 3, false), F = sla::decay_parts(g, 3, true);
     float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
     int32_t* zero = status;
     // S^T for dq (b, c = v, k), R for dv and, read across, for dk
@@ -883,10 +885,10 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
     sla::DecayStart s_start{state_in, false}, r_start{dstate_out, false};
     sla::DecayRole Rs = Rq;
     if (need_r) {
-      SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, P, g, status, zero, s));
       const sla::DecayScanJob scans[2] = {{rsums, dstate_out, dstate_in, false, true},
                                           {sums, state_in, nullptr, true, false}};
-      SLA_CUDA(sla::launch_decay_scan_parts(scans, need_s ? 2 : 1, log_decay, lens, P, g, s));
+      SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, F, g, status, zero, s));
+      SLA_CUDA(sla::launch_decay_scan_parts(scans, need_s ? 2 : 1, log_decay, lens, F, g, s));
       r_start = {rsums, true};
       zero = nullptr;
     }
@@ -894,9 +896,9 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
       s_start = {sums, true};
       Rs.transposed = false;
     }
-    SLA_CUDA(sla::launch_decay_out_tc(dout, v, k, log_decay, lens, s_start, dq, P, Rs, g, status, zero, s));
-    SLA_CUDA(sla::launch_decay_out_tc(v, dout, q, log_decay, lens, r_start, dk, P, Rk, g, status, nullptr, s));
-    SLA_CUDA(sla::launch_decay_out_tc(k, q, dout, log_decay, lens, r_start, dv, P, Rv, g, status, nullptr, s));
+    const void* tensors[] = {q, k, v, dout, dq, dk, dv};
+    const sla::DecayOut outs[3] = {{3, 2, 1, 4, s_start, Rs}, {2, 3, 0, 5, r_start, Rk}, {1, 0, 3, 6, r_start, Rv}};
+    SLA_CUDA(sla::launch_decay_out_tc(tensors, 7, outs, 3, log_decay, lens, P, F, g, status, zero, s));
     return SLA_OK;
   }
   const sla::DecayPlan P = decay_plan(g);
