@@ -225,13 +225,39 @@ struct SumsSmem {
   static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM
 };
 
+struct SumsArgs {
+  CUtensorMap maps[4];   // b, c of each job
+  SumsRole role[2];
+  float* sums[2];
+  int jobs;              // one after the other in every CTA
+  DecayParts P;
+  const float* log_decay;
+  const int32_t* lens;
+  int32_t* status;
+  int32_t* zero;
+  long long limit;
+  int withhold;
+};
+// The heads of a CTA's part, job by job.
+struct Walk {
+  const SumsArgs& A;
+  int bh0, bh1, job, bh;
+  __device__ __forceinline__ Walk(const SumsArgs& a, int first, int last)
+      : A(a), bh0(first), bh1(last), job(0), bh(first) {}
+  __device__ __forceinline__ bool on() const { return job < A.jobs; }
+  __device__ __forceinline__ void next() {
+    if (++bh > bh1) {
+      bh = bh0;
+      ++job;
+    }
+  }
+  // against the direction of the job's own walk
+  __device__ __forceinline__ bool back() const { return A.role[job].reverse == 0; }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kSumThreads, 1)
-    decay_sums_tc(const __grid_constant__ CUtensorMap mb0, const __grid_constant__ CUtensorMap mc0,
-                  const __grid_constant__ CUtensorMap mb1, const __grid_constant__ CUtensorMap mc1,
-                  const float* __restrict__ log_decay, const int32_t* __restrict__ lens,
-                  float* __restrict__ sums0, float* __restrict__ sums1, DecayParts P, SumsRole R0,
-                  SumsRole R1, int32_t* status, int32_t* zero, long long limit, int withhold) {
+    decay_sums_tc(const __grid_constant__ SumsArgs A) {
   using L = SumsSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1k(smem_raw);
@@ -249,14 +275,11 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   float* pw = reinterpret_cast<float*>(base + L::off_tab);  // decay^k by place in a step, per head parity
   const int tid = threadIdx.x, warp = tid / 32;
   const int part = blockIdx.x;
-  const bool second = blockIdx.y != 0;
-  const SumsRole R = second ? R1 : R0;
-  const CUtensorMap* mb = second ? &mb1 : &mb0;
-  const CUtensorMap* mc = second ? &mc1 : &mc0;
-  if (zero && tid == 0 && part == 0 && !second) *zero = 0;
+  const DecayParts& P = A.P;
+  const int32_t* const lens = A.lens;
+  if (A.zero && tid == 0 && part == 0) *A.zero = 0;
   const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
   const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
-  const bool rev = R.reverse == 0;  // against the direction of the walk
   if (tid == 0) {
     for (int x = 0; x < 12; ++x) mbar_init(smem_u32(bars + x), 1);
     for (int x = 0; x < 2; ++x) {
@@ -281,19 +304,21 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   // buffer q at 128 q: T at columns 0 .. 63, over 16 tokens' columns their hi
   // (8) and lo parts (8); lo2 at 64 .. 95.  Accumulators at 256 and 384
   const uint32_t tmem = *tslot;
-  const Waiter wait{status, abort_flag, limit};
+  const Waiter wait{A.status, abort_flag, A.limit};
   const unsigned all = 0xffffffffu;
   bool ok = true;
 
   if (warp == 16) {
     if (tid % 32 == 0) {
       int s = 0, ph = 1, j = 0;
-      for (int bh = bh0; ok && bh <= bh1; ++bh) {
-        const Piece<kT> pc = get_piece<kT>(P, lens, part, bh, rev);
+      for (Walk w(A, bh0, bh1); ok && w.on(); w.next()) {
+        const int bh = w.bh;
+        const CUtensorMap *mb = &A.maps[2 * w.job], *mc = mb + 1;
+        const Piece<kT> pc = get_piece<kT>(P, lens, part, bh, w.back());
         for (int i = 0; i < pc.count; ++i, ++j) {
           if (j >= L::stages && !(ok = wait(b_empty + 8 * s, ph))) break;
           mbar_expect_tx(b_full + 8 * s, L::stage);
-          if (!(withhold && j == 0 && part == 0))
+          if (!(A.withhold && j == 0 && part == 0))
             load_tile<D>(sb + s * L::stage, mb, pc.row(i), bh, b_full + 8 * s, L::half);
           load_tile<D>(sb + s * L::stage + L::tile, mc, pc.row(i), bh, b_full + 8 * s, L::half);
           if (++s == L::stages) { s = 0; ph ^= 1; }
@@ -307,8 +332,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     const uint64_t eye = eye_desc(sb + L::off_eye), db0 = sdesc(sb, L::half, 1024);
     int s = 0, ph = 0, j = 0;
     uint32_t clears = 0;        // bit q: parity of group q's next clearing
-    for (int bh = bh0; ok && bh <= bh1; ++bh) {
-      const Piece<kT> pc = uniform(get_piece<kT>(P, lens, part, bh, rev));
+    for (Walk w(A, bh0, bh1); ok && w.on(); w.next()) {
+      const Piece<kT> pc = uniform(get_piece<kT>(P, lens, part, w.bh, w.back()));
       for (int i = 0; i < pc.count; ++i, ++j) {
         const int q = j & 1;
         if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
@@ -334,8 +359,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     const uint64_t dc0 = sdesc(sb + L::tile, L::half, 1024);
     int j = 0, m = 0, s = 0, ph = 0;
-    for (int bh = bh0; ok && bh <= bh1; ++bh) {
-      const int count = uniform(get_piece<kT>(P, lens, part, bh, rev).count);
+    for (Walk w(A, bh0, bh1); ok && w.on(); w.next()) {
+      const int count = uniform(get_piece<kT>(P, lens, part, w.bh, w.back()).count);
       for (int i = 0; i < count; ++i, ++j) {
         const int place = i % kFlush, q = j & 1;
         if (place == 0 && m >= 2 &&
@@ -392,9 +417,10 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       pending = false;
       return true;
     };
-    for (int bh = bh0; bh <= bh1; ++bh) {
-      const Piece<kT> pc = get_piece<kT>(P, lens, part, bh, rev);
-      const double l2 = decay_log2(log_decay[bh % P.H]);
+    for (Walk w(A, bh0, bh1); w.on(); w.next()) {
+      const SumsRole R = A.role[w.job];
+      const Piece<kT> pc = get_piece<kT>(P, lens, part, w.bh, w.back());
+      const double l2 = decay_log2(A.log_decay[w.bh % P.H]);
       // the group's own table of decay^(place in a full step); every warp
       // comes here, also one whose wait gave up
       float* tab = pw + 2 * kT * group;
@@ -431,9 +457,9 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             reg_fence<32>(v);
             // the table counts whole steps; a partial one of the forward ends
             // early on the near side
-            const float* w = tab + 32 * h + (R.reverse ? 0 : kT - nc);
+            const float* wt = tab + 32 * h + (R.reverse ? 0 : kT - nc);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] *= far_w * w[x];
+            for (int x = 0; x < 32; ++x) v[x] *= far_w * wt[x];
             // the 16 columns read take hi and lo of their tokens
 #pragma unroll
             for (int c = 0; c < 32; c += 16) {
@@ -460,7 +486,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       if (ok && pending) ok = flush();
       // units of 4 columns, rows adjacent (the packed layout of the workspace)
       if (ok && row < D) {
-        float4* dst = reinterpret_cast<float4*>(second ? sums1 : sums0) + i64(pc.index) * (D * D / 4);
+        float4* dst = reinterpret_cast<float4*>(A.sums[w.job]) + i64(pc.index) * (D * D / 4);
 #pragma unroll
         for (int x = 0; x < CW; x += 4)
           dst[(col0 + x) / 4 * D + row] = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
@@ -975,21 +1001,26 @@ DecayParts decay_parts(const Geom& g, int jobs, bool sums) {
 cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* log_decay,
                                  const int32_t* lens, const DecayParts& P, const Geom& g,
                                  int32_t* status, int32_t* zero, cudaStream_t s) {
-  CUtensorMap m[4];
-  SumsRole r[2];
-  for (int i = 0; i < 2; ++i) {
-    const DecaySums& j = jobs[i < count ? i : 0];
-    if (!token_map(&m[2 * i], j.b, g, kT) || !token_map(&m[2 * i + 1], j.c, g, kT)) return cudaErrorInvalidValue;
-    r[i] = SumsRole{j.w_sum, j.e, j.reverse ? 1 : 0};
+  SumsArgs A{};
+  for (int i = 0; i < count; ++i) {
+    const DecaySums& j = jobs[i];
+    if (!token_map(&A.maps[2 * i], j.b, g, kT) || !token_map(&A.maps[2 * i + 1], j.c, g, kT))
+      return cudaErrorInvalidValue;
+    A.role[i] = SumsRole{j.w_sum, j.e, j.reverse ? 1 : 0};
+    A.sums[i] = j.sums;
   }
-  const int hold = debug_withhold(g, SLA_WITHHOLD_SUMMARIES) ? 1 : 0;
+  A.jobs = count;
+  A.P = P;
+  A.log_decay = log_decay;
+  A.lens = lens;
+  A.status = status;
+  A.zero = zero;
+  A.limit = wait_limit(g);
+  A.withhold = debug_withhold(g, SLA_WITHHOLD_SUMMARIES) ? 1 : 0;
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(P.parts, count), kSumThreads, smem, s>>>(m[0], m[1], m[2], m[3], log_decay, lens, jobs[0].sums,
-                                                      jobs[count - 1].sums, P, r[0], r[1], status, zero,
-                                                      wait_limit(g), hold);
-    return cudaGetLastError();
+    return launch_behind(false, kern, dim3(P.parts), kSumThreads, smem, s, A);
   };
   return g.d == 128 ? go(decay_sums_tc<128>, SumsSmem<128>::total) : go(decay_sums_tc<64>, SumsSmem<64>::total);
 }
