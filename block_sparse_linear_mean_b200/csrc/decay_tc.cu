@@ -183,8 +183,10 @@ __device__ __forceinline__ void take_part(float* v, uint32_t* part) {
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
     part[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
-    v[2 * x] -= lo_bf16(part[x]);
-    v[2 * x + 1] -= hi_bf16(part[x]);
+    const uint32_t minus = part[x] ^ 0x80008000u;
+    const float2 y = add2(make_float2(v[2 * x], v[2 * x + 1]), make_float2(lo_bf16(minus), hi_bf16(minus)));
+    v[2 * x] = y.x;
+    v[2 * x + 1] = y.y;
   }
 }
 
@@ -220,8 +222,8 @@ struct SumsSmem {
   static constexpr int stages = 6;
   static constexpr uint32_t off_eye = stages * stage;
   static constexpr uint32_t off_bar = off_eye + kEyeBytes;
-  static constexpr uint32_t off_tab = off_bar + 256;       // of both groups: 64 weights, 64 zeros
-  static constexpr uint32_t used = off_tab + 1024 + 1024;
+  static constexpr uint32_t off_tab = off_bar + 256;       // 64 weights, 64 zeros
+  static constexpr uint32_t used = off_tab + 512 + 1024;
   static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM
 };
 
@@ -268,11 +270,11 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   const uint32_t b_ready = smem_u32(bars + 14);  // [2] parts in TMEM
   const uint32_t b_acc = smem_u32(bars + 16);    // [2] an accumulation is complete
   const uint32_t b_flush = smem_u32(bars + 18);  // [2] and has been read
-  const uint32_t b_clear = smem_u32(bars + 20);  // [2] rows behind the end cleared, by group
-  const uint32_t b_used = smem_u32(bars + 22);   // [2] parts multiplied
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 24);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 25);
-  float* pw = reinterpret_cast<float*>(base + L::off_tab);  // decay^k by place in a step, per head parity
+  const uint32_t b_used = smem_u32(bars + 20);   // [2] parts multiplied
+  const uint32_t b_clear = smem_u32(bars + 22);  // rows behind the end cleared
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 23);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 24);
+  float* tab = reinterpret_cast<float*>(base + L::off_tab);
   const int tid = threadIdx.x, warp = tid / 32;
   const int part = blockIdx.x;
   const DecayParts& P = A.P;
@@ -284,12 +286,12 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     for (int x = 0; x < 12; ++x) mbar_init(smem_u32(bars + x), 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(b_t + 8 * x, 1);
-      mbar_init(b_ready + 8 * x, 8);
+      mbar_init(b_ready + 8 * x, 16);
       mbar_init(b_acc + 8 * x, 1);
       mbar_init(b_flush + 8 * x, 16);
-      mbar_init(b_clear + 8 * x, 8);
       mbar_init(b_used + 8 * x, 1);
     }
+    mbar_init(b_clear, 16);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -330,17 +332,13 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     constexpr uint32_t id_t = idesc_bf16(128, 16, 1, 0);
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     const uint64_t eye = eye_desc(sb + L::off_eye), db0 = sdesc(sb, L::half, 1024);
-    int s = 0, ph = 0, j = 0;
-    uint32_t clears = 0;        // bit q: parity of group q's next clearing
+    int s = 0, ph = 0, j = 0, clears = 0;
     for (Walk w(A, bh0, bh1); ok && w.on(); w.next()) {
       const Piece<kT> pc = uniform(get_piece<kT>(P, lens, part, w.bh, w.back()));
       for (int i = 0; i < pc.count; ++i, ++j) {
         const int q = j & 1;
         if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
-        if (pc.size(i) < kT) {
-          if (!(ok = __all_sync(all, wait(b_clear + 8 * q, clears >> q & 1)))) break;
-          clears ^= 1u << q;
-        }
+        if (pc.size(i) < kT && !(ok = __all_sync(all, wait(b_clear, clears++ & 1)))) break;
         // the parts in this buffer have been multiplied
         if (j >= 2 && !(ok = __all_sync(all, wait(b_used + 8 * q, ((j >> 1) & 1) ^ 1)))) break;
         tc_fence_after();
@@ -388,11 +386,11 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       }
     }
   } else {
-    const int quad = warp & 3, group = warp >> 3, h = warp >> 2 & 1;
+    const int quad = warp & 3, h = warp >> 2;  // rows 32 quad .., tokens 16 h .. (T), a quarter of the sum's columns
     const uint32_t lane = static_cast<uint32_t>(quad * 32) << 16;
     const int row = tid & 127;
     constexpr int CW = D / 4;      // columns of the sum that a thread keeps
-    const int col0 = (warp >> 2) * CW;
+    const int col0 = h * CW;
     const bool mine = D == 128 || quad < 2;
     float acc[CW];
     int j = 0, m = 0, s = 0, ph = 0;
@@ -421,14 +419,12 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       const SumsRole R = A.role[w.job];
       const Piece<kT> pc = get_piece<kT>(P, lens, part, w.bh, w.back());
       const double l2 = decay_log2(A.log_decay[w.bh % P.H]);
-      // the group's own table of decay^(place in a full step); every warp
-      // comes here, also one whose wait gave up
-      float* tab = pw + 2 * kT * group;
-      if (!(ok = bar_sync_and(1 + group, 256, ok))) break;
-      const int k = tid & 255;
-      if (k < kT) tab[k] = decay_power(l2, R.reverse ? k : kT - 1 - k);
-      else if (k < 2 * kT) tab[k] = 0.f;
-      asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory");
+      // the table: decay^(place in a full step); every warp comes here, also
+      // one whose wait gave up
+      if (!(ok = bar_sync_and(1, 512, ok))) break;
+      if (tid < kT) tab[tid] = decay_power(l2, R.reverse ? tid : kT - 1 - tid);
+      else if (tid < 2 * kT) tab[tid] = 0.f;
+      asm volatile("bar.sync 1, 512;" ::: "memory");
 #pragma unroll
       for (int x = 0; x < CW; ++x) acc[x] = 0.f;
       // weight of a step's near edge, toward the leaving side: the steps come
@@ -436,48 +432,61 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       double far = R.w_sum * decay_power(l2, R.e);
       const double fall = exp2(fmax(l2 * kT, -2000.0));
       for (int i = 0; ok && i < pc.count; ++i, ++j) {
-        if ((j & 1) == group) {
-          const int nc = pc.size(i);
-          const float far_w = static_cast<float>(far);
-          const uint32_t tT = tmem + 128 * group + lane;
-          if (nc < kT) {
-            if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
-            uint8_t* bt = base + s * L::stage;
-            clear_rows<D, kT>(bt, bt + L::tile, nc, tid & 255, 256);
-            fence_async_smem();
-            __syncwarp();
-            if (tid % 32 == 0) mbar_arrive(b_clear + 8 * group);
-          }
-          if (!(ok = __all_sync(all, wait(b_t + 8 * group, (j >> 1) & 1)))) break;
-          tc_fence_after();
-          if (mine) {
-            float v[32];
-            tmem_ld32(tT + 32 * h, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
-            // the table counts whole steps; a partial one of the forward ends
-            // early on the near side
-            const float* wt = tab + 32 * h + (R.reverse ? 0 : kT - nc);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] *= far_w * wt[x];
-            // the 16 columns read take hi and lo of their tokens
-#pragma unroll
-            for (int c = 0; c < 32; c += 16) {
-              uint32_t p[8];
-              const uint32_t t = tT + 32 * h + c;
-              take_part(v + c, p);
-              tmem_st8u(t, p);
-              take_part(v + c, p);
-              tmem_st8u(t + 8, p);
-              take_part(v + c, p);
-              tmem_st8u(tT + 64 + 16 * h + c / 2, p);
-            }
-            tmem_wait_st();
-          }
-          tc_fence_before();
+        const int nc = pc.size(i), q = j & 1;
+        const float far_w = static_cast<float>(far);
+        const uint32_t tT = tmem + 128 * q + lane;
+        if (nc < kT) {
+          if (!(ok = __all_sync(all, wait(b_full + 8 * s, ph)))) break;
+          uint8_t* bt = base + s * L::stage;
+          clear_rows<D, kT>(bt, bt + L::tile, nc, tid, 512);
+          fence_async_smem();
           __syncwarp();
-          if (tid % 32 == 0) mbar_arrive(b_ready + 8 * group);
+          if (tid % 32 == 0) mbar_arrive(b_clear);
         }
+        if (!(ok = __all_sync(all, wait(b_t + 8 * q, (j >> 1) & 1)))) break;
+        tc_fence_after();
+        if (mine) {
+          float v[16];
+          uint32_t p[8];
+          tmem_ld16(tT + 16 * h, v);
+          const float2 fw = make_float2(far_w, far_w);
+          // the table counts whole steps; a partial one of the forward ends
+          // early on the near side
+          float2 w[8];
+          if (R.reverse || nc == kT) {
+#pragma unroll
+            for (int x = 0; x < 8; x += 2) {
+              const float4 y = *reinterpret_cast<const float4*>(tab + 16 * h + 2 * x);
+              w[x] = make_float2(y.x, y.y);
+              w[x + 1] = make_float2(y.z, y.w);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float* y = tab + 16 * h + 2 * x + kT - nc;
+              w[x] = make_float2(y[0], y[1]);
+            }
+          }
+          tmem_wait_ld();
+          reg_fence<16>(v);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float2 y = mul2(make_float2(v[2 * x], v[2 * x + 1]), mul2(fw, w[x]));
+            v[2 * x] = y.x;
+            v[2 * x + 1] = y.y;
+          }
+          // the 16 columns read take hi and lo of their tokens
+          take_part(v, p);
+          tmem_st8u(tT + 16 * h, p);
+          take_part(v, p);
+          tmem_st8u(tT + 16 * h + 8, p);
+          take_part(v, p);
+          tmem_st8u(tT + 64 + 8 * h, p);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (tid % 32 == 0) mbar_arrive(b_ready + 8 * q);
         far *= pc.size(i) == kT ? fall : exp2(l2 * pc.size(i));
         if (pending && !(ok = flush())) break;
         pending = i % kFlush == kFlush - 1 || i + 1 == pc.count;
