@@ -64,7 +64,7 @@ __device__ __forceinline__ void add_outer(float* S, const float* b, const float*
       acc[x][4 * y] = times(f, s.x); acc[x][4 * y + 1] = times(f, s.y);
       acc[x][4 * y + 2] = times(f, s.z); acc[x][4 * y + 3] = times(f, s.w);
     }
-#pragma unroll 2
+#pragma unroll 4
   for (int r = 0; r < kC; ++r) {
     float cv[CY * 4];
     const float wr = w[r];
@@ -88,12 +88,21 @@ __device__ __forceinline__ void add_outer(float* S, const float* b, const float*
           make_float4(acc[x][4 * y], acc[x][4 * y + 1], acc[x][4 * y + 2], acc[x][4 * y + 3]);
 }
 
-// S from / to global [D][D], transposed if asked
+// S from global [D][D], transposed if asked
 template <int D>
 __device__ __forceinline__ void load_state(float* S, const float* src, bool transposed) {
-  for (int u = threadIdx.x; u < D * D; u += kThr) {
-    const int r = u / D, c = u % D;
-    S[(transposed ? c : r) * (D + 4) + (transposed ? r : c)] = src ? src[u] : 0.f;
+#pragma unroll 4
+  for (int u = threadIdx.x; u < D * D / 4; u += kThr) {
+    const int r = u / (D / 4), c = u % (D / 4) * 4;
+    const float4 f = src ? *reinterpret_cast<const float4*>(src + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (transposed) {
+      S[c * (D + 4) + r] = f.x;
+      S[(c + 1) * (D + 4) + r] = f.y;
+      S[(c + 2) * (D + 4) + r] = f.z;
+      S[(c + 3) * (D + 4) + r] = f.w;
+    } else {
+      *reinterpret_cast<float4*>(S + r * (D + 4) + c) = f;
+    }
   }
 }
 
@@ -104,6 +113,7 @@ __global__ void __launch_bounds__(kThr) decay_sums_simt(const T* __restrict__ b,
                                                         const int32_t* __restrict__ lens,
                                                         float* __restrict__ sums, DecayPlan P, int e,
                                                         bool reverse, float w_sum, int32_t* zero) {
+  next_may_launch();
   zero_word(zero);
   extern __shared__ float sm[];
   float* S = sm;
@@ -141,6 +151,7 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
                                                        const float* starts, i64 start_stride,
                                                        T* __restrict__ out, float* final_state,
                                                        DecayPlan P, DecayRole R, int32_t* zero) {
+  next_may_launch();
   zero_word(zero);
   extern __shared__ float sm[];
   constexpr int LD = D + 4;
@@ -154,9 +165,11 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
   const double l2 = decay_log2(log_decay[bh % P.H]);
   const int t0 = seg * P.seg_len, n = segment_tokens(P, lens, bh / P.H, seg);
   const i64 base = i64(bh) * P.N * D;
-  load_state<D>(S, starts ? starts + i64(bh) * start_stride + i64(seg) * D * D : nullptr, R.transposed);
   if (threadIdx.x <= kC) pw[threadIdx.x] = decay_power(l2, threadIdx.x);
-  const float2 full = decay_power2(l2, kC);
+  const bool moves = n > kC || final_state;  // whether the state is taken on at all
+  const float2 full = moves ? decay_power2(l2, kC) : make_float2(0.f, 0.f);
+  wait_for_previous();
+  load_state<D>(S, starts ? starts + i64(bh) * start_stride + i64(seg) * D * D : nullptr, R.transposed);
   for (int i0 = 0; i0 < n; i0 += kC) {
     __syncthreads();
     load_rows<T, D>(a + base, at, i0, n, t0, R.reverse);
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
     {
       const int j = threadIdx.x % 32, r = threadIdx.x / 32;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
       for (int k = 0; k < D; k += 4) {
         const float4 y = *reinterpret_cast<const float4*>(bt + j * LD + k);
 #pragma unroll
@@ -194,6 +208,7 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
       float4 y[X], z[X];
 #pragma unroll
       for (int x = 0; x < X; ++x) y[x] = z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int j = 0; j < kC; ++j) {
         const float4 v = *reinterpret_cast<const float4*>(ct + j * LD + col);
 #pragma unroll
@@ -203,6 +218,7 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
           y[x].z = fmaf(p, v.z, y[x].z); y[x].w = fmaf(p, v.w, y[x].w);
         }
       }
+#pragma unroll 4
       for (int k = 0; k < D; ++k) {
         const float4 v = *reinterpret_cast<const float4*>(S + k * LD + col);
 #pragma unroll
@@ -223,6 +239,7 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
         }
       }
     }
+    if (i0 + kC >= n && !final_state) break;  // nobody reads the state behind this chunk
     __syncthreads();
     add_outer<D>(S, bt, ct, w, nc == kC ? full : decay_power2(l2, nc));
   }
@@ -408,8 +425,9 @@ cudaError_t out_simt(const T* a, const T* b, const T* c, const float* ld, const 
   auto kern = decay_out_simt<T, D>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (err != cudaSuccess) return err;
-  kern<<<dim3(P.segs, BH), kThr, smem, s>>>(a, b, c, ld, lens, starts, stride, out, fin, P, R, zero);
-  return cudaGetLastError();
+  // (the first kernel of a call clears the status word)
+  return launch_behind(!zero, kern, dim3(P.segs, BH), kThr, smem, s, a, b, c, ld, lens, starts, stride, out,
+                       fin, P, R, zero);
 }
 
 }  // namespace
@@ -451,7 +469,7 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
 
 cudaError_t launch_decay_scan(const DecayScanJob& job, const float* log_decay, const int32_t* lens,
                               const DecayPlan& P, const Geom& g, cudaStream_t s) {
-  return launch_behind(false, decay_scan_kernel<UniformSegments>, dim3(g.d * g.d / 512, g.BH), 128, 0, s,
+  return launch_behind(true, decay_scan_kernel<UniformSegments>, dim3(g.d * g.d / 512, g.BH), 128, 0, s,
                        job, job, log_decay, lens, UniformSegments{P}, g.d);
 }
 
