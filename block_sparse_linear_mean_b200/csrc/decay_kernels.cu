@@ -26,7 +26,6 @@ namespace sla {
 
 namespace {
 
-constexpr int kC = 32;        // tokens per chunk of the fp32 kernels
 constexpr int kThr = 256;
 
 // The workspace's status word, cleared by the first kernel of a call.
@@ -34,12 +33,20 @@ __device__ __forceinline__ void zero_word(int32_t* w) {
   if (w && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *w = 0;
 }
 
-// Rows [r0, r0 + kC) (by counted index i within the piece of n tokens at t0)
+// Two neighbours as one store.
+__device__ __forceinline__ void store2(float* p, float a, float b) {
+  *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+
+// Rows [r0, r0 + C) (by counted index i within the piece of n tokens at t0)
 // of one head's [N, d] tensor into smem as fp32; rows at or past n are zero.
-template <typename T, int D>
+template <typename T, int D, int C>
 __device__ __forceinline__ void load_rows(const T* __restrict__ x, float* dst, int i0, int n, int t0,
                                           bool reverse) {
-  for (int u = threadIdx.x; u < kC * (D / 4); u += kThr) {
+  for (int u = threadIdx.x; u < C * (D / 4); u += kThr) {
     const int r = u / (D / 4), c = (u % (D / 4)) * 4;
     const int i = i0 + r;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -48,44 +55,41 @@ __device__ __forceinline__ void load_rows(const T* __restrict__ x, float* dst, i
   }
 }
 
-// S (smem, [D][D + 4]) <- f S + sum over the chunk's rows of w_r b_r^T c_r;
-// each thread owns D * D / 256 elements: rows ty + 16 x, columns 4 tx + 64 y
+// acc (a thread's E x E elements of S: rows E ty + x, columns 4 tx + 64 y + z)
+// += sum over the chunk's rows of w_r b_r^T c_r.  Two b values per row of a
+// warp and one c row: the products wait for no load (6 shared-memory cycles
+// for 64 products at D = 128).
 template <int D>
-__device__ __forceinline__ void add_outer(float* S, const float* b, const float* c, const float* w,
-                                          float2 f) {
+__device__ __forceinline__ void add_outer(float (&acc)[D / 16][D / 16], const float* b, const float* c,
+                                          const float* w, int rows) {
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  constexpr int LD = D + 4, RX = D / 16, CY = D / 64;
-  float acc[RX][CY * 4];
-#pragma unroll
-  for (int x = 0; x < RX; ++x)
-#pragma unroll
-    for (int y = 0; y < CY; ++y) {
-      const float4 s = *reinterpret_cast<const float4*>(S + (ty + 16 * x) * LD + 4 * tx + 64 * y);
-      acc[x][4 * y] = times(f, s.x); acc[x][4 * y + 1] = times(f, s.y);
-      acc[x][4 * y + 2] = times(f, s.z); acc[x][4 * y + 3] = times(f, s.w);
-    }
-#pragma unroll 4
-  for (int r = 0; r < kC; ++r) {
-    float cv[CY * 4];
+  constexpr int LD = D + 4, E = D / 16;
+#pragma unroll 2
+  for (int r = 0; r < rows; ++r) {
     const float wr = w[r];
+    float cv[E], bv[E];
 #pragma unroll
-    for (int y = 0; y < CY; ++y) {
-      const float4 v = *reinterpret_cast<const float4*>(c + r * LD + 4 * tx + 64 * y);
-      cv[4 * y] = wr * v.x; cv[4 * y + 1] = wr * v.y; cv[4 * y + 2] = wr * v.z; cv[4 * y + 3] = wr * v.w;
+    for (int y = 0; y < E; y += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(c + r * LD + 4 * tx + 16 * y);
+      cv[y] = wr * v.x; cv[y + 1] = wr * v.y; cv[y + 2] = wr * v.z; cv[y + 3] = wr * v.w;
+      const float4 u = *reinterpret_cast<const float4*>(b + r * LD + E * ty + y);
+      bv[y] = u.x; bv[y + 1] = u.y; bv[y + 2] = u.z; bv[y + 3] = u.w;
     }
 #pragma unroll
-    for (int x = 0; x < RX; ++x) {
-      const float bv = b[r * LD + ty + 16 * x];
+    for (int x = 0; x < E; ++x)
 #pragma unroll
-      for (int y = 0; y < CY * 4; ++y) acc[x][y] = fmaf(bv, cv[y], acc[x][y]);
-    }
+      for (int y = 0; y < E; ++y) acc[x][y] = fmaf(bv[x], cv[y], acc[x][y]);
   }
+}
+// A thread's elements of S: 4 consecutive columns at a time.
+template <int D, typename F>
+__device__ __forceinline__ void each_quad(F f) {
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  constexpr int E = D / 16;
 #pragma unroll
-  for (int x = 0; x < RX; ++x)
+  for (int x = 0; x < E; ++x)
 #pragma unroll
-    for (int y = 0; y < CY; ++y)
-      *reinterpret_cast<float4*>(S + (ty + 16 * x) * LD + 4 * tx + 64 * y) =
-          make_float4(acc[x][4 * y], acc[x][4 * y + 1], acc[x][4 * y + 2], acc[x][4 * y + 3]);
+    for (int y = 0; y < E; y += 4) f(x, y, E * ty + x, 4 * tx + 16 * y);
 }
 
 // S from global [D][D], transposed if asked
@@ -107,7 +111,7 @@ __device__ __forceinline__ void load_state(float* S, const float* src, bool tran
 }
 
 // (1) sums of the segments: sums[bh][seg] = w_sum sum_i e^{g (n-1-i+e)} b_i^T c_i
-template <typename T, int D>
+template <typename T, int D, int C>
 __global__ void __launch_bounds__(kThr) decay_sums_simt(const T* __restrict__ b, const T* __restrict__ c,
                                                         const float* __restrict__ log_decay,
                                                         const int32_t* __restrict__ lens,
@@ -116,34 +120,35 @@ __global__ void __launch_bounds__(kThr) decay_sums_simt(const T* __restrict__ b,
   next_may_launch();
   zero_word(zero);
   extern __shared__ float sm[];
-  float* S = sm;
-  float* bt = S + D * (D + 4);
-  float* ct = bt + kC * (D + 4);
-  __shared__ float w[kC];
+  float* bt = sm;
+  float* ct = bt + C * (D + 4);
+  __shared__ float w[C];
   const int bh = blockIdx.y, seg = blockIdx.x;
   const double l2 = decay_log2(log_decay[bh % P.H]);
   const int t0 = seg * P.seg_len, n = segment_tokens(P, lens, bh / P.H, seg);
   const i64 base = i64(bh) * P.N * D;
-  load_state<D>(S, nullptr, false);
-  for (int i0 = 0; i0 < n; i0 += kC) {
+  float acc[D / 16][D / 16] = {};
+  for (int i0 = 0; i0 < n; i0 += C) {
     __syncthreads();
-    load_rows<T, D>(b + base, bt, i0, n, t0, reverse);
-    load_rows<T, D>(c + base, ct, i0, n, t0, reverse);
+    load_rows<T, D, C>(b + base, bt, i0, n, t0, reverse);
+    load_rows<T, D, C>(c + base, ct, i0, n, t0, reverse);
     // weights count from the segment's end: nothing is scaled again later
-    if (threadIdx.x < kC) {
+    if (threadIdx.x < C) {
       const int left = n - 1 - i0 - static_cast<int>(threadIdx.x);
       w[threadIdx.x] = left >= 0 ? w_sum * decay_power(l2, left + e) : 0.f;
     }
     __syncthreads();
-    add_outer<D>(S, bt, ct, w, make_float2(1.f, 0.f));
+    add_outer<D>(acc, bt, ct, w, min(C, n - i0));
   }
-  __syncthreads();
   float* dst = sums + (i64(bh) * P.segs + seg) * D * D;
-  for (int u = threadIdx.x; u < D * D; u += kThr) dst[u] = S[u / D * (D + 4) + u % D];
+  each_quad<D>([&](int x, int y, int row, int col) {
+    *reinterpret_cast<float4*>(dst + row * D + col) =
+        make_float4(acc[x][y], acc[x][y + 1], acc[x][y + 2], acc[x][y + 3]);
+  });
 }
 
 // (3) outputs of a segment
-template <typename T, int D>
+template <typename T, int D, int C>
 __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, const T* __restrict__ b,
                                                        const T* __restrict__ c,
                                                        const float* __restrict__ log_decay,
@@ -154,94 +159,120 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
   next_may_launch();
   zero_word(zero);
   extern __shared__ float sm[];
-  constexpr int LD = D + 4;
+  constexpr int LD = D + 4, LP = C + 4, E = D / 16, Q = C / 16, W = C / 8;
   float* S = sm;
   float* at = S + D * LD;
-  float* bt = at + kC * LD;
-  float* ct = bt + kC * LD;
-  float* pt = ct + kC * LD;  // [kC][kC + 1]
-  __shared__ float w[kC], pw[kC + 1];
+  float* bt = at + C * LD;
+  float* ct = bt + C * LD;
+  float* pt = ct + C * LD;  // [C][LP]
+  __shared__ float w[C], pw[C + 1];
   const int bh = blockIdx.y, seg = blockIdx.x;
   const double l2 = decay_log2(log_decay[bh % P.H]);
   const int t0 = seg * P.seg_len, n = segment_tokens(P, lens, bh / P.H, seg);
   const i64 base = i64(bh) * P.N * D;
-  if (threadIdx.x <= kC) pw[threadIdx.x] = decay_power(l2, threadIdx.x);
-  const bool moves = n > kC || final_state;  // whether the state is taken on at all
-  const float2 full = moves ? decay_power2(l2, kC) : make_float2(0.f, 0.f);
+  if (threadIdx.x <= C) pw[threadIdx.x] = decay_power(l2, threadIdx.x);
+  const bool moves = n > C || final_state;  // whether the state is taken on at all
+  const float2 full = moves ? decay_power2(l2, C) : make_float2(0.f, 0.f);
   wait_for_previous();
   load_state<D>(S, starts ? starts + i64(bh) * start_stride + i64(seg) * D * D : nullptr, R.transposed);
-  for (int i0 = 0; i0 < n; i0 += kC) {
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  for (int i0 = 0; i0 < n; i0 += C) {
     __syncthreads();
-    load_rows<T, D>(a + base, at, i0, n, t0, R.reverse);
-    load_rows<T, D>(b + base, bt, i0, n, t0, R.reverse);
-    load_rows<T, D>(c + base, ct, i0, n, t0, R.reverse);
-    const int nc = min(kC, n - i0);
-    if (threadIdx.x < kC)
+    load_rows<T, D, C>(a + base, at, i0, n, t0, R.reverse);
+    load_rows<T, D, C>(b + base, bt, i0, n, t0, R.reverse);
+    load_rows<T, D, C>(c + base, ct, i0, n, t0, R.reverse);
+    const int nc = min(C, n - i0);
+    if (threadIdx.x < C)
       w[threadIdx.x] = threadIdx.x < nc ? R.w_sum * decay_power(l2, nc - 1 - threadIdx.x + R.e) : 0.f;
     __syncthreads();
-    // scores: 4 per thread
+    // scores: rows Q ty + x, columns tx + 16 y
     {
-      const int j = threadIdx.x % 32, r = threadIdx.x / 32;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+      float acc[Q][Q] = {};
+#pragma unroll 2
       for (int k = 0; k < D; k += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(bt + j * LD + k);
+        float4 q[Q], y[Q];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float4 q = *reinterpret_cast<const float4*>(at + (r + 8 * x) * LD + k);
-          acc[x] += q.x * y.x + q.y * y.y + q.z * y.z + q.w * y.w;
+        for (int x = 0; x < Q; ++x) {
+          q[x] = *reinterpret_cast<const float4*>(at + (Q * ty + x) * LD + k);
+          y[x] = *reinterpret_cast<const float4*>(bt + (tx + 16 * x) * LD + k);
         }
+#pragma unroll
+        for (int x = 0; x < Q; ++x)
+#pragma unroll
+          for (int z = 0; z < Q; ++z)
+            acc[x][z] = fmaf(q[x].w, y[z].w, fmaf(q[x].z, y[z].z, fmaf(q[x].y, y[z].y, fmaf(q[x].x, y[z].x, acc[x][z]))));
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int i = r + 8 * x;
-        pt[i * (kC + 1) + j] = j <= i ? R.w_in * pw[i - j] * acc[x] : 0.f;
-      }
+      for (int x = 0; x < Q; ++x)
+#pragma unroll
+        for (int z = 0; z < Q; ++z) {
+          const int i = Q * ty + x, j = tx + 16 * z;
+          pt[i * LP + j] = j <= i ? R.w_in * pw[i - j] * acc[x][z] : 0.f;
+        }
     }
     __syncthreads();
-    // outputs: rows r + 8 x, 4 columns per lane and 128-wide pass
+    // outputs: a warp's W rows, D / 32 columns per lane
     {
-      constexpr int LANES = D / 4;           // lanes that cover a row
-      constexpr int RPP = kThr / LANES;      // rows per pass
-      const int col = threadIdx.x % LANES * 4, r = threadIdx.x / LANES;
-      constexpr int X = kC / RPP;
-      float4 y[X], z[X];
+      constexpr int V = D / 32;
+      const int col = threadIdx.x % 32 * V, r0 = threadIdx.x / 32 * W;
+      float y[W][V] = {};
+      // row vector m (at `ld` floats a row, `len` of them from `from`) of each
+      // of the W rows times the rows of `mat`
+      auto product = [&](const float* m, int ld, const float* mat, int len) {
+#pragma unroll 2
+        for (int k = 0; k < len; k += 4) {
+          float v[4][V];
 #pragma unroll
-      for (int x = 0; x < X; ++x) y[x] = z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int j = 0; j < kC; ++j) {
-        const float4 v = *reinterpret_cast<const float4*>(ct + j * LD + col);
+          for (int z = 0; z < 4; ++z)
 #pragma unroll
-        for (int x = 0; x < X; ++x) {
-          const float p = pt[(r + RPP * x) * (kC + 1) + j];
-          y[x].x = fmaf(p, v.x, y[x].x); y[x].y = fmaf(p, v.y, y[x].y);
-          y[x].z = fmaf(p, v.z, y[x].z); y[x].w = fmaf(p, v.w, y[x].w);
+            for (int x = 0; x < V; x += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(mat + (k + z) * LD + col + x);
+              v[z][x] = f.x;
+              v[z][x + 1] = f.y;
+            }
+#pragma unroll
+          for (int x = 0; x < W; ++x) {
+            const float4 f = *reinterpret_cast<const float4*>(m + (r0 + x) * ld + k);
+#pragma unroll
+            for (int z = 0; z < V; ++z)
+              y[x][z] = fmaf(f.w, v[3][z], fmaf(f.z, v[2][z], fmaf(f.y, v[1][z], fmaf(f.x, v[0][z], y[x][z]))));
+          }
         }
-      }
-#pragma unroll 4
-      for (int k = 0; k < D; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(S + k * LD + col);
+      };
+      product(at, LD, S, D);
 #pragma unroll
-        for (int x = 0; x < X; ++x) {
-          const float q = at[(r + RPP * x) * LD + k];
-          z[x].x = fmaf(q, v.x, z[x].x); z[x].y = fmaf(q, v.y, z[x].y);
-          z[x].z = fmaf(q, v.z, z[x].z); z[x].w = fmaf(q, v.w, z[x].w);
-        }
-      }
+      for (int x = 0; x < W; ++x) {
+        const float f = R.w_st * pw[r0 + x + 1 - R.e];
 #pragma unroll
-      for (int x = 0; x < X; ++x) {
-        const int i = i0 + r + RPP * x;
+        for (int z = 0; z < V; ++z) y[x][z] *= f;
+      }
+      product(pt, LP, ct, r0 + W);  // (columns behind the last of the W rows are zero)
+#pragma unroll
+      for (int x = 0; x < W; ++x) {
+        const int i = i0 + r0 + x;
         if (i < n) {
-          const float f = R.w_st * pw[r + RPP * x + 1 - R.e];
-          store4(out + base + i64(t0 + (R.reverse ? n - 1 - i : i)) * D + col,
-                 make_float4(y[x].x + f * z[x].x, y[x].y + f * z[x].y, y[x].z + f * z[x].z,
-                             y[x].w + f * z[x].w));
+          T* dst = out + base + i64(t0 + (R.reverse ? n - 1 - i : i)) * D + col;
+          if constexpr (V == 4) store4(dst, make_float4(y[x][0], y[x][1], y[x][2], y[x][3]));
+          else store2(dst, y[x][0], y[x][1]);
         }
       }
     }
-    if (i0 + kC >= n && !final_state) break;  // nobody reads the state behind this chunk
+    if (i0 + C >= n && !final_state) break;  // nobody reads the state behind this chunk
     __syncthreads();
-    add_outer<D>(S, bt, ct, w, nc == kC ? full : decay_power2(l2, nc));
+    {
+      const float2 f = nc == C ? full : decay_power2(l2, nc);
+      float acc[E][E];
+      each_quad<D>([&](int x, int z, int row, int col) {
+        const float4 v = *reinterpret_cast<const float4*>(S + row * LD + col);
+        acc[x][z] = times(f, v.x); acc[x][z + 1] = times(f, v.y);
+        acc[x][z + 2] = times(f, v.z); acc[x][z + 3] = times(f, v.w);
+      });
+      add_outer<D>(acc, bt, ct, w, nc);
+      each_quad<D>([&](int x, int z, int row, int col) {
+        *reinterpret_cast<float4*>(S + row * LD + col) =
+            make_float4(acc[x][z], acc[x][z + 1], acc[x][z + 2], acc[x][z + 3]);
+      });
+    }
   }
   // rows behind the sequence's end
   const int pad = min(P.seg_len, P.N - t0) - n;
@@ -405,48 +436,74 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const T* __restrict__ q
   }
 }
 
-template <typename T, int D>
-cudaError_t sums_simt(const T* b, const T* c, const float* ld, const int32_t* lens, float* sums,
-                      const DecayPlan& P, int e, bool reverse, float w_sum, int BH, int32_t* zero,
-                      cudaStream_t s) {
-  const size_t smem = sizeof(float) * (D + 2 * kC) * (D + 4);
-  auto kern = decay_sums_simt<T, D>;
+template <typename T, int D, int C>
+cudaError_t sums_simt(const DecaySums& j, const float* ld, const int32_t* lens, const DecayPlan& P, int BH,
+                      int32_t* zero, cudaStream_t s) {
+  const size_t smem = sizeof(float) * 2 * C * (D + 4);
+  auto kern = decay_sums_simt<T, D, C>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (err != cudaSuccess) return err;
-  kern<<<dim3(P.segs, BH), kThr, smem, s>>>(b, c, ld, lens, sums, P, e, reverse, w_sum, zero);
+  kern<<<dim3(P.segs, BH), kThr, smem, s>>>(static_cast<const T*>(j.b), static_cast<const T*>(j.c), ld, lens,
+                                            j.sums, P, j.e, j.reverse, j.w_sum, zero);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t out_simt(const T* a, const T* b, const T* c, const float* ld, const int32_t* lens,
-                     const float* starts, i64 stride, T* out, float* fin, const DecayPlan& P,
+template <typename T, int D, int C>
+cudaError_t out_simt(const void* a, const void* b, const void* c, const float* ld, const int32_t* lens,
+                     const float* starts, i64 stride, void* out, float* fin, const DecayPlan& P,
                      const DecayRole& R, int BH, int32_t* zero, cudaStream_t s) {
-  const size_t smem = sizeof(float) * ((D + 3 * kC) * (D + 4) + kC * (kC + 1));
-  auto kern = decay_out_simt<T, D>;
+  const size_t smem = sizeof(float) * ((D + 3 * C) * (D + 4) + C * (C + 4));
+  auto kern = decay_out_simt<T, D, C>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (err != cudaSuccess) return err;
   // (the first kernel of a call clears the status word)
-  return launch_behind(!zero, kern, dim3(P.segs, BH), kThr, smem, s, a, b, c, ld, lens, starts, stride, out,
-                       fin, P, R, zero);
+  return launch_behind(!zero, kern, dim3(P.segs, BH), kThr, smem, s, static_cast<const T*>(a),
+                       static_cast<const T*>(b), static_cast<const T*>(c), ld, lens, starts, stride,
+                       static_cast<T*>(out), fin, P, R, zero);
 }
 
 }  // namespace
 
-int decay_simt_chunk() { return kC; }
-
-cudaError_t launch_decay_sums_simt(const void* b, const void* c, const float* log_decay,
-                                   const int32_t* lens, float* sums, const DecayPlan& P, int e,
-                                   bool reverse, float w_sum, const Geom& g, int32_t* zero,
-                                   cudaStream_t s) {
-  using bf = __nv_bfloat16;
-  if (g.dtype == SLA_F32) {
-    const float *x = static_cast<const float*>(b), *y = static_cast<const float*>(c);
-    return g.d == 64 ? sums_simt<float, 64>(x, y, log_decay, lens, sums, P, e, reverse, w_sum, g.BH, zero, s)
-                     : sums_simt<float, 128>(x, y, log_decay, lens, sums, P, e, reverse, w_sum, g.BH, zero, s);
+// Chunks of 64 tokens, of 32 where 64 would leave SMs without a CTA (2 heads of
+// 1,024 tokens at d = 64: 19 us, 23 with 64; 12 heads of 8,000 at d = 128: 545
+// us, 770 with 32).  Segments: as many as run shortest, in waves of the CTAs
+// that fit the SMs (shared memory: one per SM at d = 128, two at 64).
+DecayPlan decay_plan(const Geom& g) {
+  constexpr int kSms = 148;
+  DecayPlan P;
+  P.N = g.N;
+  P.H = g.H;
+  P.chunk = i64((g.N + 63) / 64) * g.BH < kSms ? 32 : 64;
+  const int chunks = (g.N + P.chunk - 1) / P.chunk, slots = g.d == 64 ? 2 * kSms : kSms;
+  int best = 1;
+  i64 least = 0;
+  for (int segs = 1; segs <= chunks && (segs == 1 || i64(segs - 1) * g.BH < 4 * slots); ++segs) {
+    const int len = (chunks + segs - 1) / segs;
+    const i64 ctas = i64((chunks + len - 1) / len) * g.BH, waves = (ctas + slots - 1) / slots;
+    const i64 cost = waves * (len + 1);  // (a chunk's time goes by until the first is there)
+    if (segs == 1 || cost < least) {
+      least = cost;
+      best = len;
+    }
   }
-  const bf *x = static_cast<const bf*>(b), *y = static_cast<const bf*>(c);
-  return g.d == 64 ? sums_simt<bf, 64>(x, y, log_decay, lens, sums, P, e, reverse, w_sum, g.BH, zero, s)
-                   : sums_simt<bf, 128>(x, y, log_decay, lens, sums, P, e, reverse, w_sum, g.BH, zero, s);
+  if (least == i64((g.BH + slots - 1) / slots) * (chunks + 1)) best = chunks;  // one segment needs no sums
+  P.seg_len = best * P.chunk;
+  P.segs = (g.N + P.seg_len - 1) / P.seg_len;
+  return P;
+}
+
+#define SLA_DECAY_SIMT(fn, ...)                                                                       \
+  if (g.dtype == SLA_F32) {                                                                           \
+    if (P.chunk == 64) return g.d == 64 ? fn<float, 64, 64>(__VA_ARGS__) : fn<float, 128, 64>(__VA_ARGS__); \
+    return g.d == 64 ? fn<float, 64, 32>(__VA_ARGS__) : fn<float, 128, 32>(__VA_ARGS__);              \
+  }                                                                                                   \
+  if (P.chunk == 64) return g.d == 64 ? fn<bf, 64, 64>(__VA_ARGS__) : fn<bf, 128, 64>(__VA_ARGS__);   \
+  return g.d == 64 ? fn<bf, 64, 32>(__VA_ARGS__) : fn<bf, 128, 32>(__VA_ARGS__);
+
+cudaError_t launch_decay_sums_simt(const DecaySums& job, const float* log_decay, const int32_t* lens,
+                                   const DecayPlan& P, const Geom& g, int32_t* zero, cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  SLA_DECAY_SIMT(sums_simt, job, log_decay, lens, P, g.BH, zero, s)
 }
 
 cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, const float* log_decay,
@@ -454,17 +511,7 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
                                   float* final_state, const DecayPlan& P, const DecayRole& R,
                                   const Geom& g, int32_t* zero, cudaStream_t s) {
   using bf = __nv_bfloat16;
-  if (g.dtype == SLA_F32) {
-    const float *x = static_cast<const float*>(a), *y = static_cast<const float*>(b),
-                *z = static_cast<const float*>(c);
-    float* o = static_cast<float*>(out);
-    return g.d == 64 ? out_simt<float, 64>(x, y, z, log_decay, lens, starts, start_stride, o, final_state, P, R, g.BH, zero, s)
-                     : out_simt<float, 128>(x, y, z, log_decay, lens, starts, start_stride, o, final_state, P, R, g.BH, zero, s);
-  }
-  const bf *x = static_cast<const bf*>(a), *y = static_cast<const bf*>(b), *z = static_cast<const bf*>(c);
-  bf* o = static_cast<bf*>(out);
-  return g.d == 64 ? out_simt<bf, 64>(x, y, z, log_decay, lens, starts, start_stride, o, final_state, P, R, g.BH, zero, s)
-                   : out_simt<bf, 128>(x, y, z, log_decay, lens, starts, start_stride, o, final_state, P, R, g.BH, zero, s);
+  SLA_DECAY_SIMT(out_simt, a, b, c, log_decay, lens, starts, start_stride, out, final_state, P, R, g.BH, zero, s)
 }
 
 cudaError_t launch_decay_scan(const DecayScanJob& job, const float* log_decay, const int32_t* lens,

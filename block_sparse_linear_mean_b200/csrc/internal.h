@@ -245,6 +245,7 @@ cudaError_t launch_rotary(const Geom& g, const sla_rotary& r, const i64* raw_str
 // roles and segments are).
 struct DecayPlan {
   int N, H;
+  int chunk;          // tokens that a CTA takes together
   int seg_len, segs;  // tokens per segment (a multiple of the chunk), segments
 };
 struct DecayRole {
@@ -253,12 +254,18 @@ struct DecayRole {
   bool reverse;             // last token to first
   bool transposed;          // the stored state is the transpose of the one used
 };
-// `zero`, if given, is a status word that the launch clears.
-int decay_simt_chunk();
-cudaError_t launch_decay_sums_simt(const void* b, const void* c, const float* log_decay,
-                                   const int32_t* lens, float* sums, const DecayPlan& P, int e,
-                                   bool reverse, float w_sum, const Geom& g, int32_t* zero,
-                                   cudaStream_t s);
+struct DecaySums {
+  const void *b, *c;
+  float* sums;
+  float w_sum;
+  int e;
+  bool reverse;
+};
+DecayPlan decay_plan(const Geom& g);  // segments of the fp32 kernels
+// `zero`, if given, is a status word that the launch, the first of a call,
+// clears.
+cudaError_t launch_decay_sums_simt(const DecaySums& job, const float* log_decay, const int32_t* lens,
+                                   const DecayPlan& P, const Geom& g, int32_t* zero, cudaStream_t s);
 cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, const float* log_decay,
                                   const int32_t* lens, const float* starts, i64 start_stride, void* out,
                                   float* final_state, const DecayPlan& P, const DecayRole& R,
@@ -285,13 +292,6 @@ struct DecayParts {
 // Parts of a launch of the output kernel with `jobs` roles, or of the sums
 // that go with it (finer where there are chunks enough, cuts at the same places).
 DecayParts decay_parts(const Geom& g, int jobs, bool sums);
-struct DecaySums {
-  const void *b, *c;
-  float* sums;
-  float w_sum;
-  int e;
-  bool reverse;
-};
 cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* log_decay,
                                  const int32_t* lens, const DecayParts& P, const Geom& g,
                                  int32_t* status, int32_t* zero, cudaStream_t s);

@@ -173,26 +173,12 @@ BwdWs bwd_ws(const Geom& g) {
   return w;
 }
 
-// Segments of the fp32 kernels of the decayed linear attention: enough (head,
-// segment) pairs for two waves of one CTA per SM, whole chunks each.
-sla::DecayPlan decay_plan(const Geom& g) {
-  const int chunk = sla::decay_simt_chunk();
-  const int chunks = (g.N + chunk - 1) / chunk;
-  const int want = std::min(chunks, std::max(1, (2 * 148 + g.BH - 1) / g.BH));
-  sla::DecayPlan P;
-  P.N = g.N;
-  P.H = g.H;
-  P.seg_len = (chunks + want - 1) / want * chunk;
-  P.segs = (g.N + P.seg_len - 1) / P.seg_len;
-  return P;
-}
-
 DecayWs decay_ws(const Geom& g, bool backward) {
   size_t states;  // in the workspace of one set of sums
   if (sla::decay_tc_supported(g)) {
     states = size_t(sla::decay_parts(g, backward ? 3 : 1, true).parts) + g.BH;
   } else {
-    const sla::DecayPlan P = decay_plan(g);
+    const sla::DecayPlan P = sla::decay_plan(g);
     states = P.segs > 1 ? size_t(g.BH) * P.segs : 0;
   }
   states *= sizeof(float) * g.d * g.d;
@@ -827,13 +813,13 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     SLA_CUDA(sla::launch_decay_out_tc(tensors, 4, &job, 1, log_decay, lens, P, P, g, status, zero, s));
     return SLA_OK;
   }
-  const sla::DecayPlan P = decay_plan(g);
+  const sla::DecayPlan P = sla::decay_plan(g);
   if (P.segs == 1) {
     SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, state_in, int64_t(g.d) * g.d, out,
                                         state_out, P, R, g, status, s));
     return SLA_OK;
   }
-  SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
+  SLA_CUDA(sla::launch_decay_sums_simt({k, v, sums, 1.0f, 0, false}, log_decay, lens, P, g, status, s));
   SLA_CUDA(sla::launch_decay_scan({sums, state_in, state_out, false, false}, log_decay, lens, P, g, s));
   SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, sums, int64_t(P.segs) * g.d * g.d, out,
                                       nullptr, P, R, g, nullptr, s));
@@ -901,16 +887,16 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
     SLA_CUDA(sla::launch_decay_out_tc(tensors, 7, outs, 3, log_decay, lens, P, F, g, status, zero, s));
     return SLA_OK;
   }
-  const sla::DecayPlan P = decay_plan(g);
+  const sla::DecayPlan P = sla::decay_plan(g);
   const int64_t one = int64_t(g.d) * g.d;
   const float *s0 = state_in, *r0 = dstate_out;
   int64_t stride = one;
   float* fin = dstate_in;
   if (P.segs > 1) {
     float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
-    SLA_CUDA(sla::launch_decay_sums_simt(k, v, log_decay, lens, sums, P, 0, false, 1.0f, g, status, s));
+    SLA_CUDA(sla::launch_decay_sums_simt({k, v, sums, 1.0f, 0, false}, log_decay, lens, P, g, status, s));
     SLA_CUDA(sla::launch_decay_scan({sums, state_in, nullptr, false, false}, log_decay, lens, P, g, s));
-    SLA_CUDA(sla::launch_decay_sums_simt(q, dout, log_decay, lens, rsums, P, 1, true, g.scale, g, nullptr, s));
+    SLA_CUDA(sla::launch_decay_sums_simt({q, dout, rsums, g.scale, 1, true}, log_decay, lens, P, g, nullptr, s));
     SLA_CUDA(sla::launch_decay_scan({rsums, dstate_out, dstate_in, false, true}, log_decay, lens, P, g, s));
     s0 = sums;
     r0 = rsums;
