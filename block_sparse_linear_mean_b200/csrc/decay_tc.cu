@@ -138,12 +138,39 @@ __device__ __forceinline__ Piece<T> uniform(Piece<T> x) {
   return x;
 }
 
+// L2 eviction policies: what nobody reads again goes first, so that what the
+// sums read last stays for the output kernel.
+__device__ __forceinline__ uint64_t l2_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t l2_normal() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // A [rows][D] tile as D / 64 swizzled halves of `half` bytes each.
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int row, int bh,
-                                          uint32_t bar, uint32_t half) {
+                                          uint32_t bar, uint32_t half, uint64_t policy) {
 #pragma unroll
-  for (int h = 0; h < D / 64; ++h) tma_load_3d(dst + h * half, map, h * 64, row, bh, bar);
+  for (int h = 0; h < D / 64; ++h)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst + h * half),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(h * 64), "r"(row), "r"(bh), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src, int x, int y, int z,
+                                           uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src), "l"(policy)
+      : "memory");
 }
 
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -207,6 +234,7 @@ constexpr int kThreads = 576;      // 16 worker warps, loader, issuer
 constexpr int kSumThreads = 608;   // ... and two issuers
 constexpr int kT = 64;             // tokens per step
 constexpr int kFlush = 4;          // steps per accumulation
+constexpr int kKept = 18;          // steps at a piece's entering side that are left in L2 (148 x 18 x 32 KB)
 
 struct SumsRole {
   float w_sum;
@@ -240,16 +268,16 @@ struct SumsArgs {
   long long limit;
   int withhold;
 };
-// The heads of a CTA's part, job by job.
+// The heads of a CTA's part, job by job, the output kernel's first one last.
 struct Walk {
   const SumsArgs& A;
   int bh0, bh1, job, bh;
   __device__ __forceinline__ Walk(const SumsArgs& a, int first, int last)
-      : A(a), bh0(first), bh1(last), job(0), bh(first) {}
+      : A(a), bh0(first), bh1(last), job(0), bh(last) {}
   __device__ __forceinline__ bool on() const { return job < A.jobs; }
   __device__ __forceinline__ void next() {
-    if (++bh > bh1) {
-      bh = bh0;
+    if (--bh < bh0) {
+      bh = bh1;
       ++job;
     }
   }
@@ -312,6 +340,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 
   if (warp == 16) {
     if (tid % 32 == 0) {
+      const uint64_t first = l2_first(), normal = l2_normal();
       int s = 0, ph = 1, j = 0;
       for (Walk w(A, bh0, bh1); ok && w.on(); w.next()) {
         const int bh = w.bh;
@@ -320,9 +349,10 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         for (int i = 0; i < pc.count; ++i, ++j) {
           if (j >= L::stages && !(ok = wait(b_empty + 8 * s, ph))) break;
           mbar_expect_tx(b_full + 8 * s, L::stage);
+          const uint64_t policy = pc.count - i > kKept ? first : normal;
           if (!(A.withhold && j == 0 && part == 0))
-            load_tile<D>(sb + s * L::stage, mb, pc.row(i), bh, b_full + 8 * s, L::half);
-          load_tile<D>(sb + s * L::stage + L::tile, mc, pc.row(i), bh, b_full + 8 * s, L::half);
+            load_tile<D>(sb + s * L::stage, mb, pc.row(i), bh, b_full + 8 * s, L::half, policy);
+          load_tile<D>(sb + s * L::stage + L::tile, mc, pc.row(i), bh, b_full + 8 * s, L::half, policy);
           if (++s == L::stages) { s = 0; ph ^= 1; }
         }
       }
@@ -635,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
   if (warp == 16) {
     if (tid % 32 == 0) {
       const CUtensorMap *ma = &A.maps[J.a], *mb = &A.maps[J.b], *mc = &A.maps[J.c];
+      const uint64_t policy = A.jobs == 1 ? l2_first() : l2_normal();  // (roles share tensors)
       int j = 0;
       for (int bh = bh0; ok && bh <= bh1; ++bh) {
         const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, rev);
@@ -645,12 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
           const uint32_t st = sb + s * L::stage, bar = b_full + 8 * s, ph = ((j >> 1) & 1) ^ 1;
           if (j >= 2 && !(ok = wait(b_eb + 8 * s, ph))) break;
           mbar_expect_tx(bar, 2 * L::tile);
-          load_tile<D>(st + L::tile, mb, pc.row(i), bh, bar, 16384);
+          load_tile<D>(st + L::tile, mb, pc.row(i), bh, bar, 16384, policy);
           if (j >= 2 && !(ok = wait(b_ea + 8 * s, ph))) break;
-          if (!(A.withhold && j == 0 && blockIdx.x == 0)) load_tile<D>(st, ma, pc.row(i), bh, bar, 16384);
+          if (!(A.withhold && j == 0 && blockIdx.x == 0)) load_tile<D>(st, ma, pc.row(i), bh, bar, 16384, policy);
           if (j >= 2 && !(ok = wait(b_ec + 8 * s, ph))) break;
           mbar_expect_tx(b_fc + 8 * s, L::tile);
-          load_tile<D>(st + 2 * L::tile, mc, pc.row(i), bh, b_fc + 8 * s, 16384);
+          load_tile<D>(st + 2 * L::tile, mc, pc.row(i), bh, b_fc + 8 * s, 16384, policy);
         }
       }
     }
@@ -878,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
     }
   } else {
     // ------------------------------------------------ results
+    const uint64_t policy = l2_first();
     int j = 0;
     for (int bh = bh0; bh <= bh1; ++bh) {
       const Piece<kC> pc = get_piece<kC>(P, lens, part, bh, rev);
@@ -950,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
         if (r == 0) {
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_store_3d(&A.maps[J.o], sb + s * L::stage + 2 * L::tile + h * 16384, h * 64, pc.row(i), bh);
+            store_tile(&A.maps[J.o], sb + s * L::stage + 2 * L::tile + h * 16384, h * 64, pc.row(i), bh, policy);
           tma_store_commit();
           tma_store_wait_read();
           mbar_arrive(b_ec + 8 * s);

@@ -303,3 +303,128 @@ def test_refusals():
         sla.decay_attention(p, x, x, x, g, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(sla.SlaError):
         sla.decay_attention_step(p, x, x, x, g, torch.zeros(1, 2, 64, 64, device="cuda"))
+
+
+def _long_reference(q, k, v, g, scale):
+    """out and state of one head in 64 bits on the GPU, rows 512 at a time."""
+    q, k, v = q.double(), k.double(), v.double()
+    n = q.shape[0]
+    t = torch.arange(n, device=q.device, dtype=torch.float64)
+    out = torch.empty_like(q)
+    for a in range(0, n, 512):
+        b = min(n, a + 512)
+        gap = t[a:b, None] - t[None, :b]
+        w = torch.where(gap >= 0, torch.exp(g * gap.clamp(min=0)), 0.0)
+        out[a:b] = scale * ((q[a:b] @ k[:b].T) * w) @ v[:b]
+    return out, (k * torch.exp(g * (n - 1 - t))[:, None]).T @ v
+
+
+@pytest.mark.parametrize("B,H,N,d,dtype", [(1, 2, 20011, 128, BF), (1, 5, 9001, 64, BF), (1, 2, 9001, 128, F32)])
+def test_long_sequences(B, H, N, d, dtype):
+    """Heads cut into many pieces; sums over thousands of tokens keep the
+    states' accuracy (a chain of products left in one tensor-core accumulator
+    over such a length loses 2^-17)."""
+    q, k, v = (randn(40 + i, B, H, N, d, dtype=dtype) for i in range(3))
+    g = torch.log1p(-torch.exp2(-torch.linspace(8, 13, H))).cuda()
+    f = sla.decay_attention(sla.token_params(B, H, N, d, dtype), q, k, v, g)
+    rel = 2.0 ** -17 if dtype == F32 else 3 * 2.0 ** -8
+    for h in range(H):
+        out, S = _long_reference(q[0, h], k[0, h], v[0, h], g[h].double(), d ** -0.5)
+        assert torch.linalg.norm(f["out"][0, h].double() - out) <= rel * torch.linalg.norm(out)
+        assert torch.linalg.norm(f["state"][0, h].double() - S) <= 2.0 ** -19 * torch.linalg.norm(S)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_partial_chunk_per_head_many_heads(dtype):
+    """More heads than CTAs, each a few tokens: every CTA goes over many
+    pieces that begin and end with a partial chunk."""
+    B, H, N, d = 37, 9, 33, 128
+    q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, dtype, None, True, "usual")
+    lens = [(7 * b) % 34 for b in range(B)]
+    lt = torch.tensor(lens, dtype=torch.int32).cuda()
+    out, S = tok.decay_forward(q, k, v, g.cpu(), lens, s0)
+    grads = tok.decay_backward(q, k, v, g.cpu(), do, lens, s0, ds)
+    (mo, ms), mg = magnitude(q, k, v, do, s0, ds, g, lens)
+    poison(lens, q, k, v, do)
+    p = sla.token_params(B, H, N, d, dtype)
+    f = sla.decay_attention(p, q, k, v, g, lens=lt, state=s0)
+    b = sla.decay_attention_backward(p, q, k, v, g, do, lens=lt, state=s0, dstate=ds)
+    assert sla.check_device_status(f["ws"]) == sla.SLA_OK
+    assert sla.check_device_status(b["ws"]) == sla.SLA_OK
+    near(f["out"], out, mo, dtype, dtype == BF, "out")
+    state_near(f["state"], S, ms, "state")
+    for name, want, mag in zip(("dq", "dk", "dv"), grads, mg):
+        near(b[name], want, mag, dtype, dtype == BF, name)
+    state_near(b["dstate"], grads[3], mg[3], "dstate")
+
+
+@pytest.mark.parametrize("B,H", [(49, 3), (37, 4)])  # no head cut in the backward, in the forward
+def test_whole_heads_without_a_state_to_hand_on(B, H):
+    """The C entry with state_out, dstate_in NULL: heads that no CTA shares
+    need no sums, the given states are read where they stand (and across, for
+    dq and dk)."""
+    N, d = 200, 128
+    q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, BF, None, True, "usual")
+    p = sla.token_params(B, H, N, d, BF)
+    full = sla.decay_attention(p, q, k, v, g, state=s0)
+    fb = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds)
+    out, dq, dk, dv = (torch.empty_like(q) for _ in range(4))
+    ws = sla.workspace(p, sla.SLA_OP_DECAY_BACKWARD, "cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    P = lambda t: t.data_ptr()  # noqa: E731
+    assert sla.sla_decay_attention(p, P(q), P(k), P(v), P(g), None, P(s0), P(out), None, P(ws), ws.numel(),
+                                   s) == sla.SLA_OK
+    assert sla.check_device_status(ws) == sla.SLA_OK
+    assert sla.sla_decay_attention_backward(p, P(q), P(k), P(v), P(g), None, P(s0), P(do), P(ds), P(dq), P(dk),
+                                            P(dv), None, P(ws), ws.numel(), s) == sla.SLA_OK
+    assert sla.check_device_status(ws) == sla.SLA_OK
+    want, _ = tok.decay_forward(q, k, v, g.cpu(), None, s0)
+    grads = tok.decay_backward(q, k, v, g.cpu(), do, None, s0, ds)
+    (mo, _), mg = magnitude(q, k, v, do, s0, ds, g, None)
+    near(out, want, mo, BF, True, "out")
+    for t, w, m, name in zip((dq, dk, dv), grads, mg, ("dq", "dk", "dv")):
+        near(t, w, m, BF, True, name)
+    # the same sums behind the same products: equal to the calls with states
+    assert torch.equal(out, full["out"]) or torch.linalg.norm(out.float() - full["out"].float()) <= 2.0 ** -8 * torch.linalg.norm(full["out"].float())
+    assert torch.linalg.norm(dv.float() - fb["dv"].float()) <= 2.0 ** -8 * torch.linalg.norm(fb["dv"].float())
+
+
+def test_two_streams_at_once():
+    B, H, N, d = 1, 12, 3000, 128
+    one = inputs(B, H, N, d, BF, None, True, "usual")
+    sets = [one, (one[2], one[0], one[1], one[3], one[5], one[4], None, one[7])]
+    p = sla.token_params(B, H, N, d, BF)
+    want = [sla.decay_attention_backward(p, x[0], x[1], x[2], x[7], x[3], state=x[4], dstate=x[5]) for x in sets]
+    wf = [sla.decay_attention(p, *x[:3], x[7], state=x[4]) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for rep in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                x = sets[i]
+                f = sla.decay_attention(p, x[0], x[1], x[2], x[7], state=x[4])
+                got[i] = sla.decay_attention_backward(p, x[0], x[1], x[2], x[7], x[3], state=x[4], dstate=x[5]), f
+    torch.cuda.synchronize()
+    for (b, f), w, y in zip(got, want, wf):
+        assert sla.check_device_status(b["ws"]) == sla.SLA_OK
+        assert torch.equal(f["out"], y["out"]) and torch.equal(f["state"], y["state"])
+        for n in ("dq", "dk", "dv", "dstate"):
+            assert torch.equal(b[n], w[n])
+
+
+def test_gradient_state_in_place():
+    B, H, N, d = 2, 3, 500, 128
+    for dtype in (BF, F32):
+        q, k, v, do, s0, ds, _, g = inputs(B, H, N, d, dtype, None, True, "usual")
+        p = sla.token_params(B, H, N, d, dtype)
+        want = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds)
+        dq, dk, dv, both = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q), ds.clone()
+        ws = sla.workspace(p, sla.SLA_OP_DECAY_BACKWARD, "cuda")
+        P = lambda t: t.data_ptr()  # noqa: E731
+        assert sla.sla_decay_attention_backward(
+            p, P(q), P(k), P(v), P(g), None, P(s0), P(do), P(both), P(dq), P(dk), P(dv), P(both), P(ws),
+            ws.numel(), torch.cuda.current_stream().cuda_stream) == sla.SLA_OK
+        torch.cuda.synchronize()
+        for got, name in ((dq, "dq"), (dk, "dk"), (dv, "dv"), (both, "dstate")):
+            assert torch.equal(got, want[name]), (dtype, name)

@@ -1,0 +1,50 @@
+"""Failure path of the decayed linear attention's tensor-core kernels: a
+withheld tile load makes every wait give up after a bounded time, the status
+word says so, and the next call is as good as ever."""
+
+import pytest
+import torch
+
+from block_sparse_linear_mean_b200 import sla
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(B=1, H=3, N=700, d=128, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    q, k, v, do = (torch.randn(B, H, N, d, generator=g).to(torch.bfloat16).cuda() for _ in range(4))
+    return q, k, v, do, torch.log1p(-torch.exp2(-torch.linspace(3, 8, H))).cuda()
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("kernel", [sla.SLA_WITHHOLD_ATTENTION, sla.SLA_WITHHOLD_SUMMARIES])
+@pytest.mark.parametrize("backward", [False, True])
+def test_withheld_load_is_reported(d, kernel, backward):
+    q, k, v, do, g = _inputs(d=d)
+    p = sla.token_params(*q.shape, torch.bfloat16)
+
+    def call():
+        if backward:
+            return sla.decay_attention_backward(p, q, k, v, g, do)
+        return sla.decay_attention(p, q, k, v, g)
+
+    want = call()
+    p.flags = sla.SLA_FLAG_DEBUG_TIMEOUT | sla.SLA_DEBUG_WITHHOLD(kernel)
+    bad = call()
+    torch.cuda.synchronize()
+    assert sla.check_device_status(bad["ws"]) == sla.SLA_ERR_TIMEOUT
+    p.flags = 0
+    again = call()
+    assert sla.check_device_status(again["ws"]) == sla.SLA_OK
+    for name in ("dq", "dk", "dv", "dstate") if backward else ("out", "state"):
+        assert torch.equal(again[name], want[name])
+
+
+def test_other_withheld_kernels_leave_these_calls_alone():
+    q, k, v, do, g = _inputs()
+    p = sla.token_params(*q.shape, torch.bfloat16)
+    want = sla.decay_attention(p, q, k, v, g)
+    p.flags = sla.SLA_FLAG_DEBUG_TIMEOUT | sla.SLA_DEBUG_WITHHOLD(sla.SLA_WITHHOLD_BWD_DQ)
+    got = sla.decay_attention(p, q, k, v, g)
+    assert sla.check_device_status(got["ws"]) == sla.SLA_OK
+    assert torch.equal(got["out"], want["out"])
