@@ -475,18 +475,19 @@ DecayPlan decay_plan(const Geom& g) {
   P.H = g.H;
   P.chunk = i64((g.N + 63) / 64) * g.BH < kSms ? 32 : 64;
   const int chunks = (g.N + P.chunk - 1) / P.chunk, slots = g.d == 64 ? 2 * kSms : kSms;
-  int best = 1;
+  int best = chunks;
   i64 least = 0;
   for (int segs = 1; segs <= chunks && (segs == 1 || i64(segs - 1) * g.BH < 4 * slots); ++segs) {
     const int len = (chunks + segs - 1) / segs;
     const i64 ctas = i64((chunks + len - 1) / len) * g.BH, waves = (ctas + slots - 1) / slots;
-    const i64 cost = waves * (len + 1);  // (a chunk's time goes by until the first is there)
+    // a chunk's time goes by until the first is there; more than one segment
+    // adds the sums (two fifths of the work) and the scan
+    const i64 cost = segs == 1 ? 10 * waves * (len + 1) : 14 * waves * (len + 1) + 25;
     if (segs == 1 || cost < least) {
       least = cost;
       best = len;
     }
   }
-  if (least == i64((g.BH + slots - 1) / slots) * (chunks + 1)) best = chunks;  // one segment needs no sums
   P.seg_len = best * P.chunk;
   P.segs = (g.N + P.seg_len - 1) / P.seg_len;
   return P;

@@ -259,6 +259,10 @@ struct SumsArgs {
   CUtensorMap maps[4];   // b, c of each job
   SumsRole role[2];
   float* sums[2];
+  // Heads that no CTA shares: no scan follows, the sums go with the state at
+  // the sequence's entering side (null: zeros) straight to the one behind it.
+  const float* first[2];
+  float* last[2];
   int jobs;              // one after the other in every CTA
   DecayParts P;
   const float* log_decay;
@@ -523,12 +527,27 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         if (++s == L::stages) { s = 0; ph ^= 1; }
       }
       if (ok && pending) ok = flush();
-      // units of 4 columns, rows adjacent (the packed layout of the workspace)
       if (ok && row < D) {
-        float4* dst = reinterpret_cast<float4*>(A.sums[w.job]) + i64(pc.index) * (D * D / 4);
+        if (float* last = A.last[w.job]) {
+          const i64 at = i64(w.bh) * D * D + row * D + col0;
+          const float* first = A.first[w.job];
+          const float2 f = decay_power2(l2, pc.tokens);
 #pragma unroll
-        for (int x = 0; x < CW; x += 4)
-          dst[(col0 + x) / 4 * D + row] = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
+          for (int x = 0; x < CW; x += 4) {
+            float4 y = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
+            if (first) {
+              const float4 z = *reinterpret_cast<const float4*>(first + at + x);
+              y.x += times(f, z.x); y.y += times(f, z.y); y.z += times(f, z.z); y.w += times(f, z.w);
+            }
+            *reinterpret_cast<float4*>(last + at + x) = y;
+          }
+        } else {
+          // units of 4 columns, rows adjacent (the packed layout of the workspace)
+          float4* dst = reinterpret_cast<float4*>(A.sums[w.job]) + i64(pc.index) * (D * D / 4);
+#pragma unroll
+          for (int x = 0; x < CW; x += 4)
+            dst[(col0 + x) / 4 * D + row] = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
+        }
       }
     }
   }
@@ -1049,6 +1068,8 @@ cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* 
       return cudaErrorInvalidValue;
     A.role[i] = SumsRole{j.w_sum, j.e, j.reverse ? 1 : 0};
     A.sums[i] = j.sums;
+    A.first[i] = j.first;
+    A.last[i] = j.last;
   }
   A.jobs = count;
   A.P = P;

@@ -260,6 +260,10 @@ struct DecaySums {
   float w_sum;
   int e;
   bool reverse;
+  // tensor cores only: with `last`, and heads that no part cuts, the state
+  // behind the sequence is formed here, from the one before it (nullable)
+  const float* first = nullptr;
+  float* last = nullptr;
 };
 DecayPlan decay_plan(const Geom& g);  // segments of the fp32 kernels
 // `zero`, if given, is a status word that the launch, the first of a call,

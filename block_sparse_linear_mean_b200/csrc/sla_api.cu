@@ -795,15 +795,14 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
   float* sums = at<float>(ws, w.sums);
   if (sla::decay_tc_supported(g)) {
     // the state that is handed on, to the next piece of a head or to the
-    // caller, comes from the sums kernel, which keeps it to fp32 accuracy;
-    // whole heads and no state wanted need no sums
+    // caller, comes from the sums kernel, which keeps it to fp32 accuracy
     const sla::DecayParts P = sla::decay_parts(g, 1, false);
     sla::DecayStart start{state_in, false};
     int32_t* zero = status;
-    if (!whole_heads(P) || state_out) {
+    if (!whole_heads(P)) {
       const sla::DecaySums job{k, v, sums, 1.0f, 0, false};
-      SLA_CUDA(sla::launch_decay_sums_tc(&job, 1, log_decay, lens, P, g, status, zero, s));
       const sla::DecayScanJob scan{sums, state_in, state_out, false, false};
+      SLA_CUDA(sla::launch_decay_sums_tc(&job, 1, log_decay, lens, P, g, status, zero, s));
       SLA_CUDA(sla::launch_decay_scan_parts(&scan, 1, log_decay, lens, P, g, s));
       start = {sums, true};
       zero = nullptr;
@@ -811,6 +810,10 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     const void* tensors[] = {q, k, v, out};
     const sla::DecayOut job{0, 1, 2, 3, start, R};
     SLA_CUDA(sla::launch_decay_out_tc(tensors, 4, &job, 1, log_decay, lens, P, P, g, status, zero, s));
+    if (whole_heads(P) && state_out) {  // (behind the outputs, which read state_in: it may be state_out)
+      const sla::DecaySums last{k, v, nullptr, 1.0f, 0, false, state_in, state_out};
+      SLA_CUDA(sla::launch_decay_sums_tc(&last, 1, log_decay, lens, P, g, status, nullptr, s));
+    }
     return SLA_OK;
   }
   const sla::DecayPlan P = sla::decay_plan(g);
@@ -867,24 +870,26 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
     int32_t* zero = status;
     // S^T for dq (b, c = v, k), R for dv and, read across, for dk
     const sla::DecaySums jobs[2] = {{q, dout, rsums, g.scale, 1, true}, {v, k, sums, 1.0f, 0, false}};
-    const bool need_s = !whole_heads(P), need_r = need_s || dstate_in;
+    const bool cut = !whole_heads(P);
     sla::DecayStart s_start{state_in, false}, r_start{dstate_out, false};
     sla::DecayRole Rs = Rq;
-    if (need_r) {
+    if (cut) {
       const sla::DecayScanJob scans[2] = {{rsums, dstate_out, dstate_in, false, true},
                                           {sums, state_in, nullptr, true, false}};
-      SLA_CUDA(sla::launch_decay_sums_tc(jobs, need_s ? 2 : 1, log_decay, lens, F, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan_parts(scans, need_s ? 2 : 1, log_decay, lens, F, g, s));
+      SLA_CUDA(sla::launch_decay_sums_tc(jobs, 2, log_decay, lens, F, g, status, zero, s));
+      SLA_CUDA(sla::launch_decay_scan_parts(scans, 2, log_decay, lens, F, g, s));
       r_start = {rsums, true};
-      zero = nullptr;
-    }
-    if (need_s) {
       s_start = {sums, true};
       Rs.transposed = false;
+      zero = nullptr;
     }
     const void* tensors[] = {q, k, v, dout, dq, dk, dv};
     const sla::DecayOut outs[3] = {{3, 2, 1, 4, s_start, Rs}, {2, 3, 0, 5, r_start, Rk}, {1, 0, 3, 6, r_start, Rv}};
     SLA_CUDA(sla::launch_decay_out_tc(tensors, 7, outs, 3, log_decay, lens, P, F, g, status, zero, s));
+    if (!cut && dstate_in) {  // (behind the gradients, which read dstate_out: it may be dstate_in)
+      const sla::DecaySums last{q, dout, nullptr, g.scale, 1, true, dstate_out, dstate_in};
+      SLA_CUDA(sla::launch_decay_sums_tc(&last, 1, log_decay, lens, P, g, status, nullptr, s));
+    }
     return SLA_OK;
   }
   const sla::DecayPlan P = sla::decay_plan(g);
