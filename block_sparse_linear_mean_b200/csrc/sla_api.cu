@@ -173,6 +173,13 @@ BwdWs bwd_ws(const Geom& g) {
   return w;
 }
 
+// Whether no part of the chunks cuts a head.
+bool whole_heads(const sla::DecayParts& P) {
+  for (int k = 1; k < P.parts; ++k)
+    if (P.begin(k) % P.chunks) return false;
+  return true;
+}
+
 DecayWs decay_ws(const Geom& g, bool backward) {
   size_t states;  // in the workspace of one set of sums
   if (sla::decay_tc_supported(g)) {
@@ -188,13 +195,6 @@ DecayWs decay_ws(const Geom& g, bool backward) {
   w.rsums = off; if (backward) off = align_up(off + states);
   w.total = off;
   return w;
-}
-
-// Whether no part of the chunks cuts a head.
-bool whole_heads(const sla::DecayParts& P) {
-  for (int k = 1; k < P.parts; ++k)
-    if (P.begin(k) % P.chunks) return false;
-  return true;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

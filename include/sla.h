@@ -431,7 +431,9 @@ SLA_API sla_status sla_apply_rotary(const sla_params* p, const sla_rotary* r,
  *   state_out  [B,H,d,d] fp32 out, nullable: the state behind each sequence's
  *              last real token (state_in where it has none).  May be state_in
  * bf16 runs on the tensor cores (SLA_FLAG_SIMT selects fp32 FMAs), fp32 on
- * fp32 FMAs.  States are fp32 and keep fp32 accuracy.  p's block and mask
+ * fp32 FMAs.  States are fp32 and keep fp32 accuracy.  Tokens are taken in
+ * chunks of at most 128: an infinity or NaN in a real token may reach all
+ * tokens of its chunk, earlier ones too (behind lens[b] it reaches none).  p's block and mask
  * fields are checked but not used.  Workspace: SLA_OP_DECAY; no output may
  * overlap an input except state_out as said. */
 SLA_API sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k,

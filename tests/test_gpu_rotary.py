@@ -9,8 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from block_sparse_linear_mean_b200 import sla
-from gpu_util import to_np
+from block_sparse_linear_mean_b200 import sla, synth
+from gpu_util import gpu_inputs, to_np
 from oracle import token_ops as tok
 
 pytestmark = pytest.mark.gpu
@@ -162,6 +162,33 @@ def test_broadcast_input_and_wide_strides():
     assert torch.equal(sla.apply_rotary(p, r, x), sla.apply_rotary(p, r, x.contiguous()))
 
 
+def test_before_and_behind_the_hybrid_attention():
+    """As a video DiT runs it: q and k turned by (frame, row, column) on their
+    way from the projection's layout into tile order, mask, forward, backward,
+    and the fp32 gradients back to the projection's layout and type.  Turning
+    into an order is turning and then moving, bit for bit, and so is the way
+    back."""
+    wl = synth.small_case(d=128, grid=(2, 8, 32), H=2, dtype="bf16", frac_crit=0.25, frac_marg=0.25)
+    _, t = gpu_inputs(wl, seed=5, with_dout=True)
+    p = sla.params_from(t["q"], wl)
+    r = sla.rotary(128, layout="interleaved", axis_pairs=(22, 21, 21), grid=wl.grid)
+    perm = sla.tile_order(wl.grid, (2, 4, 8), "cuda")
+    raw = [t[n].transpose(1, 2).contiguous().transpose(1, 2) for n in ("q", "k")]  # [B, N, H, d] in memory
+    q, k = sla.apply_rotary(p, r, *raw, perm=perm)
+    for x, y in zip((q, k), sla.apply_rotary(p, r, t["q"], t["k"])):
+        assert torch.equal(x, sla.permute_tokens(p, y, perm))
+    v, do = (sla.permute_tokens(p, t[n], perm) for n in ("v", "dout"))
+    m = sla.build_mask(p, q, k, want_cols=True)
+    f = sla.forward(p, q, k, v, t["proj"], m["rows"], save_for_backward=True)
+    b = sla.backward(p, q, k, v, t["proj"], do, m["rows"], m["cols"], f)
+    assert sla.check_device_status(b["ws"]) == sla.SLA_OK
+    dq, dk = sla.apply_rotary_backward(p, r, b["dq"], b["dk"], perm=perm)
+    for got, g in ((dq, b["dq"]), (dk, b["dk"])):
+        assert got.dtype == BF and got.transpose(1, 2).is_contiguous()
+        assert torch.equal(got, sla.apply_rotary_backward(p, r, sla.permute_tokens(p, g, perm, inverse=True)))
+        assert got.isfinite().all() and got.abs().max() > 0
+
+
 def test_other_stream_and_graph():
     B, H, N, d = 1, 4, 100, 128
     p, r = sla.token_params(B, H, N, d, BF), sla.rotary(128)
@@ -172,7 +199,12 @@ def test_other_stream_and_graph():
         sla.apply_rotary(p, r, q, out=out)
     q.copy_(randn(13, B, H, N, d, dtype=BF))
     g.replay()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = sla.apply_rotary(p, r, q)
     torch.cuda.synchronize()
+    assert torch.equal(other, out)
     assert torch.equal(out, sla.apply_rotary(p, r, q)) and not torch.equal(out, want)
 
 
