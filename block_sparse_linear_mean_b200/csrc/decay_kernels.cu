@@ -465,8 +465,8 @@ cudaError_t out_simt(const void* a, const void* b, const void* c, const float* l
 }  // namespace
 
 // Chunks of 64 tokens, of 32 where 64 would leave SMs without a CTA (2 heads of
-// 1,024 tokens at d = 64: 19 us, 23 with 64; 12 heads of 8,000 at d = 128: 545
-// us, 770 with 32).  Segments: as many as run shortest, in waves of the CTAs
+// 1,024 tokens at d = 64: 14.2 us, 19.8 with 64; 12 heads of 8,000 at d = 128:
+// 452 us, 549 with 32).  Segments: as many as run shortest, in waves of the CTAs
 // that fit the SMs (shared memory: one per SM at d = 128, two at 64).
 DecayPlan decay_plan(const Geom& g) {
   constexpr int kSms = 148;

@@ -251,7 +251,8 @@ struct SumsSmem {
   static constexpr uint32_t off_eye = stages * stage;
   static constexpr uint32_t off_bar = off_eye + kEyeBytes;
   static constexpr uint32_t off_tab = off_bar + 256;       // 64 weights, 64 zeros
-  static constexpr uint32_t used = off_tab + 512 + 1024;
+  static constexpr uint32_t off_pow = off_tab + 512;       // decay over the piece
+  static constexpr uint32_t used = off_pow + 16 + 1024;
   static constexpr uint32_t total = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM
 };
 
@@ -307,6 +308,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 23);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 24);
   float* tab = reinterpret_cast<float*>(base + L::off_tab);
+  float2* const over = reinterpret_cast<float2*>(base + L::off_pow);
   const int tid = threadIdx.x, warp = tid / 32;
   const int part = blockIdx.x;
   const DecayParts& P = A.P;
@@ -334,7 +336,6 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   __syncthreads();
   tc_fence_after();
   next_may_launch();
-  wait_for_previous();
   // buffer q at 128 q: T at columns 0 .. 63, over 16 tokens' columns their hi
   // (8) and lo parts (8); lo2 at 64 .. 95.  Accumulators at 256 and 384
   const uint32_t tmem = *tslot;
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       if (!(ok = bar_sync_and(1, 512, ok))) break;
       if (tid < kT) tab[tid] = decay_power(l2, R.reverse ? tid : kT - 1 - tid);
       else if (tid < 2 * kT) tab[tid] = 0.f;
+      else if (tid == 2 * kT && A.first[w.job]) *over = decay_power2(l2, pc.tokens);
       asm volatile("bar.sync 1, 512;" ::: "memory");
 #pragma unroll
       for (int x = 0; x < CW; ++x) acc[x] = 0.f;
@@ -531,16 +533,26 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         if (float* last = A.last[w.job]) {
           const i64 at = i64(w.bh) * D * D + row * D + col0;
           const float* first = A.first[w.job];
-          const float2 f = decay_power2(l2, pc.tokens);
+          if (first) {
+            const float2 f = *over;
 #pragma unroll
-          for (int x = 0; x < CW; x += 4) {
-            float4 y = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
-            if (first) {
-              const float4 z = *reinterpret_cast<const float4*>(first + at + x);
-              y.x += times(f, z.x); y.y += times(f, z.y); y.z += times(f, z.z); y.w += times(f, z.w);
+            for (int x = 0; x < CW; x += 16) {
+              // (in one go: first may be last, so no load passes a store)
+              float4 z[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) z[y] = *reinterpret_cast<const float4*>(first + at + x + 4 * y);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                acc[x + 4 * y] += times(f, z[y].x); acc[x + 4 * y + 1] += times(f, z[y].y);
+                acc[x + 4 * y + 2] += times(f, z[y].z); acc[x + 4 * y + 3] += times(f, z[y].w);
+              }
             }
-            *reinterpret_cast<float4*>(last + at + x) = y;
           }
+          // the outputs before may read the state in this place
+          wait_for_previous();
+#pragma unroll
+          for (int x = 0; x < CW; x += 4)
+            *reinterpret_cast<float4*>(last + at + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
         } else {
           // units of 4 columns, rows adjacent (the packed layout of the workspace)
           float4* dst = reinterpret_cast<float4*>(A.sums[w.job]) + i64(pc.index) * (D * D / 4);
@@ -551,6 +563,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       }
     }
   }
+  wait_for_previous();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -1082,7 +1095,7 @@ cudaError_t launch_decay_sums_tc(const DecaySums* jobs, int count, const float* 
   auto go = [&](auto kern, uint32_t smem) {
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    return launch_behind(false, kern, dim3(P.parts), kSumThreads, smem, s, A);
+    return launch_behind(!zero, kern, dim3(P.parts), kSumThreads, smem, s, A);
   };
   return g.d == 128 ? go(decay_sums_tc<128>, SumsSmem<128>::total) : go(decay_sums_tc<64>, SumsSmem<64>::total);
 }
