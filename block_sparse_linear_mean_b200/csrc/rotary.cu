@@ -14,7 +14,11 @@
 // cosines of its few pairs of one token in registers and walks over the heads
 // of both tensors: one 64-bit angle per (token, pair), not per value.
 //
-// Bound by HBM: every value is read once and written once.
+// Bound by HBM: every value is read once and written once.  q and k of 12 heads
+// of 32,760 tokens, d = 128, bf16, from the projection's layout into tile order
+// and the dense one: 403 MB in 66 us (6.1 TB/s); gradients in fp32 back, 604 MB
+// in 92 us (6.6 TB/s).  Rows wait in the words they are stored in, not as fp32,
+// so that four CTAs fit an SM (62 registers): 99 us before that, 76 with three.
 #include <algorithm>
 
 #include "common.cuh"
@@ -105,9 +109,9 @@ struct Words {
 };
 
 // A unit is V pairs of one token's row (2 V channels); the d / (2 V) units of
-// a row take one thread each.  The first pairs / V of them turn, the rest are
-// copied.  Half layout: channels [a, a + V) and [a + pairs, + V); interleaved:
-// 2 V neighbours.
+// a row take one thread each.  The first `pairs` pairs turn, the rest are copied.
+// Half layout: channels [a, a + V) and [a + pairs, + V), and V divides `pairs`;
+// interleaved: 2 V neighbours, and a unit may turn some of its pairs only.
 template <typename TIn, typename TOut, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs A) {
   __shared__ double turns[kMaxPairs];
@@ -125,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     t = A.perm[n];
     if (t < 0 || t >= A.N) return;
   }
-  const bool turn = u * V < A.pairs;
+  const int turned = A.pairs - u * V;  // pairs of the unit that turn, if positive
+  const bool turn = turned > 0;
   float cs[V], sn[V];
   if (turn) {
     i64 pos[3];
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float a = x[k][0].get(2 * i), b = x[k][0].get(2 * i + 1);
-            y.put(2 * i, turn ? a * cs[i] - b * sn[i] : a, turn ? b * cs[i] + a * sn[i] : b);
+            y.put(2 * i, i < turned ? a * cs[i] - b * sn[i] : a, i < turned ? b * cs[i] + a * sn[i] : b);
           }
           y.store(dst + c0);
         } else {
@@ -243,18 +248,14 @@ cudaError_t launch(RotaryArgs& a, cudaStream_t s) {
 
 template <typename TIn, typename TOut>
 cudaError_t dispatch(RotaryArgs& a, bool inter, cudaStream_t s) {
-  // Pairs per unit: four where the split at `pairs` allows it (interleaved bf16
-  // moves 16 bytes per access, half layout twice 8).  q and k of 12 heads of
-  // 32,760 tokens, d = 128, bf16: 66 us in both layouts; with two pairs 79
-  // (interleaved) and 85 us (half), with eight, half, 81: fewer rows in flight.
-  constexpr bool wide = sizeof(TIn) == 2 || sizeof(TOut) == 2;
+  // Pairs per unit: four (interleaved bf16 moves 16 bytes per access, half
+  // layout twice 8), two in interleaved fp32 (16 bytes); in half layout fewer
+  // where the split at `pairs` asks for it.  q and k of 12 heads of 32,760
+  // tokens, d = 128, bf16: 66 us in both layouts; with two pairs 79
+  // (interleaved) and 85 us (half), with one 138 and 135; with eight, half, 81:
+  // fewer rows in flight.
   const int p = a.pairs;
-  if (inter) {
-    if constexpr (wide)
-      if (p % 4 == 0) return launch<TIn, TOut, 4, true>(a, s);
-    if (p % 2 == 0) return launch<TIn, TOut, 2, true>(a, s);
-    return launch<TIn, TOut, 1, true>(a, s);
-  }
+  if (inter) return launch<TIn, TOut, sizeof(TIn) == 2 || sizeof(TOut) == 2 ? 4 : 2, true>(a, s);
   if (p % 4 == 0) return launch<TIn, TOut, 4, false>(a, s);
   if (p % 2 == 0) return launch<TIn, TOut, 2, false>(a, s);
   return launch<TIn, TOut, 1, false>(a, s);

@@ -222,3 +222,26 @@ def test_refusals():
         sla.apply_rotary(p, r, q, positions=torch.zeros(8, dtype=torch.int64, device="cuda"))
     with pytest.raises(sla.SlaError):
         sla.apply_rotary(p, r, q, out=q[..., :].view(-1).view(1, 2, 8, 64), perm=torch.arange(8, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rot,d", [(42, 64), (90, 128), (126, 128), (2, 64), (6, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_channels_that_do_not_turn(layout, rot, d, dtype):
+    # copied, infinities and NaN among them (a NaN stays one, its payload is
+    # nobody's), which reach no pair beside them (a thread's unit may hold both)
+    B, H, N = 2, 3, 37
+    p, r = sla.token_params(B, H, N, d, dtype), sla.rotary(rot, layout=layout, scaling="yarn", factor=8.0)
+    w, amp = tok.rotary_frequencies([rot // 2], scaling="yarn", factor=8.0)
+    amp = float(np.float32(amp))
+    x = randn(20, B, H, N, d, dtype=dtype)
+    x[..., rot:] = torch.tensor([float("inf"), float("nan"), -float("inf"), 3.0]).to(dtype).cuda().repeat(d)[: d - rot]
+    pos = torch.arange(N, dtype=torch.int32).cuda().expand(1, N).contiguous()
+    want = tok.rotate(x[..., :rot], np.arange(N)[None], [rot // 2], w, amp, layout)
+    got = sla.apply_rotary(p, r, x, positions=pos)
+    check(got[..., :rot].contiguous(), x[..., :rot], want, rot // 2, layout, amp, dtype, "turned")
+    np.testing.assert_array_equal(to_np(got[..., rot:]), to_np(x[..., rot:]))
+    back = sla.apply_rotary_backward(p, r, x, positions=pos)
+    want = tok.rotate(x[..., :rot], np.arange(N)[None], [rot // 2], w, amp, layout, inverse=True)
+    check(back[..., :rot].contiguous(), x[..., :rot], want, rot // 2, layout, amp, dtype, "back")
+    np.testing.assert_array_equal(to_np(back[..., rot:]), to_np(x[..., rot:]))
