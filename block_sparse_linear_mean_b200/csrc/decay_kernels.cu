@@ -33,6 +33,15 @@ __device__ __forceinline__ void zero_word(int32_t* w) {
   if (w && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *w = 0;
 }
 
+// 16 bytes into shared memory, asynchronously.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Two neighbours as one store.
 __device__ __forceinline__ void store2(float* p, float a, float b) {
   *reinterpret_cast<float2*>(p) = make_float2(a, b);
@@ -140,6 +149,8 @@ __global__ void __launch_bounds__(kThr) decay_sums_simt(const T* __restrict__ b,
     __syncthreads();
     add_outer<D>(acc, bt, ct, w, min(C, n - i0));
   }
+  if (threadIdx.x == 0)  // what the scan multiplies by where it passes the segment
+    reinterpret_cast<float2*>(sums + i64(gridDim.y) * P.segs * D * D)[i64(bh) * P.segs + seg] = decay_power2(l2, n);
   float* dst = sums + (i64(bh) * P.segs + seg) * D * D;
   each_quad<D>([&](int x, int y, int row, int col) {
     *reinterpret_cast<float4*>(dst + row * D + col) =
@@ -291,86 +302,93 @@ __global__ void __launch_bounds__(kThr) decay_out_simt(const T* __restrict__ a, 
 // (2) The sums of a head's segments -> the state at each one's entering side,
 // in place; the state behind the last one -> final_state.  One thread per 4
 // elements, segments in the walk's order: sums are read and written once (they
-// sit in L2), the order of the additions is fixed.  12 heads in 160 pieces, d =
-// 128: 12 us, most of them the wait for the sums; up to 14 segments' sums are in
-// flight per thread, which covers a head of that shape in one trip to L2.
+// sit in L2), the order of the additions is fixed.  What a state falls by over
+// each segment stands behind the sums, where their kernel left it:
+// exponentials in 64 bits would be the longest part of this one.
+//
+// Bound by L2 where heads are many (280 heads of 200 tokens, d = 128, 428 pieces:
+// the whole call 63 us; with the exponentials formed here and 14 sums per thread
+// in registers 94), by the chain of segments where they are few (one head of
+// 75,600 tokens in 148 pieces: 43 us, 61).  18 heads of 2,029 lose 2 of 31 us.
 //
 // The segments are the uniform ones of the fp32 kernels, or the pieces of the
 // tensor-core kernels with their packed sums (units of 4 columns, rows
-// adjacent).  Each block first tables its head's segments: place and factor.
+// adjacent).  Of the latter only states are written that the output kernel
+// reads: its parts may be several of the sums'.
 struct UniformSegments {
   DecayPlan P;
   static constexpr bool packed = false;
+  __device__ i64 places() const { return i64(gridDim.y) * P.segs; }
   __device__ int first(int) const { return 0; }
-  __device__ int count(int) const { return P.segs; }
-  __device__ int begin(int, int i) const { return i * P.seg_len; }
-  __device__ int place(int bh, int i) const { return bh * P.segs + i; }
+  __device__ int last(int) const { return P.segs - 1; }
+  __device__ i64 place(int bh, int k) const { return i64(bh) * P.segs + k; }
+  __device__ int finer() const { return 1; }
 };
 struct PieceSegments {
   DecayParts P;
   static constexpr bool packed = true;
+  __device__ i64 places() const { return P.places(); }
   __device__ int first(int bh) const { return P.part(i64(bh) * P.chunks); }
-  __device__ int count(int bh) const { return P.part(i64(bh + 1) * P.chunks - 1) - first(bh) + 1; }
-  // first token of part k within head bh
-  __device__ int begin(int bh, int k) const {
-    return static_cast<int>(min(max(P.begin(k) - i64(bh) * P.chunks, i64(0)), i64(P.chunks))) * 128;
-  }
-  __device__ int place(int bh, int k) const { return k + bh; }
+  __device__ int last(int bh) const { return P.part(i64(bh + 1) * P.chunks - 1); }
+  __device__ i64 place(int bh, int k) const { return k + bh; }
+  // parts k with k (from behind: k + 1) a multiple of this begin one of the output kernel's
+  __device__ int finer() const { return P.finer; }
 };
 
-constexpr int kScan = 14;      // segments' sums in flight per thread
-constexpr int kScanTable = 512;  // segments of a head tabled at a time
+// A thread's sums are under way to shared memory all at once (as registers they
+// would cost occupancy where heads are many and trips to L2 where segments are),
+// up to kScan of them: two rounds for one head in 148 pieces.
+constexpr int kScan = 74;
+
 template <typename Segments>
-__global__ void __launch_bounds__(128) decay_scan_kernel(DecayScanJob j0, DecayScanJob j1,
-                                                         const float* __restrict__ log_decay,
-                                                         const int32_t* __restrict__ lens, Segments G,
-                                                         int d) {
+__global__ void __launch_bounds__(128) decay_scan_kernel(DecayScanJob j0, DecayScanJob j1, Segments G, int d,
+                                                         int room) {
   next_may_launch();
-  __shared__ float2 factor[kScanTable];
-  __shared__ int place[kScanTable];
+  extern __shared__ float4 buf[];  // [room][128], then their factors
+  float2* fac = reinterpret_cast<float2*>(buf + room * 128);
   const DecayScanJob J = blockIdx.z ? j1 : j0;
-  float4* sums = reinterpret_cast<float4*>(J.sums);
-  const int dd4 = d * d / 4;
-  const int u = blockIdx.x * 128 + threadIdx.x;
-  const int bh = blockIdx.y;
+  const int dd4 = d * d / 4, u = blockIdx.x * 128 + threadIdx.x, bh = blockIdx.y;
   const int r = G.packed ? u % d : u / (d / 4), c = G.packed ? u / d * 4 : u % (d / 4) * 4;
-  const double l2 = decay_log2(log_decay[bh % G.P.H]);
-  const int len = decay_tokens(lens, bh / G.P.H, G.P.N);
-  const int segs = G.count(bh), seg0 = G.first(bh);
+  float4* sums = reinterpret_cast<float4*>(J.sums) + u;
+  const float2* factor = reinterpret_cast<const float2*>(J.sums + G.places() * d * d);
+  const int k0 = G.first(bh), n = G.last(bh) - k0 + 1;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (J.first) {
     const float* f = J.first + i64(bh) * d * d;
     s = J.turned ? make_float4(f[c * d + r], f[(c + 1) * d + r], f[(c + 2) * d + r], f[(c + 3) * d + r])
                  : *reinterpret_cast<const float4*>(f + r * d + c);
   }
-  for (int t0 = 0; t0 < segs; t0 += kScanTable) {
-    const int tn = min(kScanTable, segs - t0);
+  const int dir = J.reverse ? -1 : 1, start = J.reverse ? k0 + n - 1 : k0;
+  const i64 step = i64(dir) * dd4;
+  float4* p = sums + G.place(bh, start) * dd4;
+  const float2* fp = factor + G.place(bh, start);
+  // steps until a state is due; one is at the head's own side
+  const int finer = G.finer(), over = (J.reverse ? start + 1 : start) % finer;
+  int due = 0, next = J.reverse ? (over ? over : finer) : finer - over;
+  wait_for_previous();
+  for (int t0 = 0; t0 < n; t0 += room) {
+    const int m = min(room, n - t0);
+    if (t0) __syncthreads();
+#pragma unroll 2
+    for (int i = 0; i < m; ++i) copy_async16(buf + i * 128 + threadIdx.x, p + i * step);
+    for (int i = threadIdx.x; i < m; i += 128) fac[i] = fp[(t0 + i) * dir];
+    wait_copies();
     __syncthreads();
-    for (int i = threadIdx.x; i < tn; i += 128) {
-      const int k = seg0 + (J.reverse ? segs - 1 - (t0 + i) : t0 + i);
-      const int b0 = G.begin(bh, k), b1 = G.begin(bh, k + 1);
-      factor[i] = decay_power2(l2, min(max(len - b0, 0), b1 - b0));
-      place[i] = G.place(bh, k);
-    }
-    __syncthreads();
-    if (t0 == 0) wait_for_previous();
-    for (int i0 = 0; i0 < tn; i0 += kScan) {
-      float4 x[kScan];
-#pragma unroll
-      for (int i = 0; i < kScan; ++i)
-        if (i0 + i < tn) x[i] = sums[i64(place[i0 + i]) * dd4 + u];
-#pragma unroll
-      for (int i = 0; i < kScan; ++i) {
-        if (i0 + i < tn) {
-          sums[i64(place[i0 + i]) * dd4 + u] = s;
-          const float2 f = factor[i0 + i];
-          s.x = fmaf(f.x, s.x, fmaf(f.y, s.x, x[i].x)); s.y = fmaf(f.x, s.y, fmaf(f.y, s.y, x[i].y));
-          s.z = fmaf(f.x, s.z, fmaf(f.y, s.z, x[i].z)); s.w = fmaf(f.x, s.w, fmaf(f.y, s.w, x[i].w));
-        }
+#pragma unroll 2
+    for (int i = 0; i < m; ++i, p += step) {
+      const float4 x = buf[i * 128 + threadIdx.x];
+      const float2 f = fac[i];
+      if (due == 0) {
+        *p = s;
+        due = next;
+        next = finer;
       }
+      --due;
+      s.x = fmaf(f.x, s.x, fmaf(f.y, s.x, x.x)); s.y = fmaf(f.x, s.y, fmaf(f.y, s.y, x.y));
+      s.z = fmaf(f.x, s.z, fmaf(f.y, s.z, x.z)); s.w = fmaf(f.x, s.w, fmaf(f.y, s.w, x.w));
     }
   }
-  if (J.last) reinterpret_cast<float4*>(J.last)[i64(bh) * dd4 + r * (d / 4) + c / 4] = s;
+  if (J.last) *reinterpret_cast<float4*>(J.last + i64(bh) * d * d + r * d + c) = s;
 }
 
 // Few tokens: the state is read and written once, by CTAs that own 32 columns
@@ -519,17 +537,26 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
   SLA_DECAY_SIMT(out_simt, a, b, c, log_decay, lens, starts, start_stride, out, final_state, P, R, g.BH, zero, s)
 }
 
-cudaError_t launch_decay_scan(const DecayScanJob& job, const float* log_decay, const int32_t* lens,
-                              const DecayPlan& P, const Geom& g, cudaStream_t s) {
-  return launch_behind(true, decay_scan_kernel<UniformSegments>, dim3(g.d * g.d / 512, g.BH), 128, 0, s,
-                       job, job, log_decay, lens, UniformSegments{P}, g.d);
+// `most`: segments of a head, at most
+template <typename Segments>
+cudaError_t launch_scan(const DecayScanJob& j0, const DecayScanJob& j1, int jobs, const Segments& G, int most,
+                        const Geom& g, cudaStream_t s) {
+  const int room = std::min(most, kScan);
+  const size_t smem = room * (128 * sizeof(float4) + sizeof(float2));
+  cudaError_t e = cudaFuncSetAttribute(decay_scan_kernel<Segments>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_behind(true, decay_scan_kernel<Segments>, dim3(g.d * g.d / 512, g.BH, jobs), 128, smem, s, j0, j1,
+                       G, g.d, room);
 }
 
-cudaError_t launch_decay_scan_parts(const DecayScanJob* jobs, int count, const float* log_decay,
-                                    const int32_t* lens, const DecayParts& P, const Geom& g,
+cudaError_t launch_decay_scan(const DecayScanJob& job, const DecayPlan& P, const Geom& g, cudaStream_t s) {
+  return launch_scan(job, job, 1, UniformSegments{P}, P.segs, g, s);
+}
+
+cudaError_t launch_decay_scan_parts(const DecayScanJob* jobs, int count, const DecayParts& P, const Geom& g,
                                     cudaStream_t s) {
-  return launch_behind(true, decay_scan_kernel<PieceSegments>, dim3(g.d * g.d / 512, g.BH, count), 128, 0,
-                       s, jobs[0], jobs[count - 1], log_decay, lens, PieceSegments{P}, g.d);
+  return launch_scan(jobs[0], jobs[count - 1], count, PieceSegments{P}, P.parts / P.BH + 2, g, s);
 }
 
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay,

@@ -325,8 +325,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   const DecayParts& P = A.P;
   const int32_t* const lens = A.lens;
   if (A.zero && tid == 0 && part == 0) *A.zero = 0;
-  const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
-  const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
+  const int bh0 = P.head(P.begin(part)), bh1 = P.head(P.begin(part + 1) - 1);
   if (tid == 0) {
     for (int x = 0; x < 12; ++x) mbar_init(smem_u32(bars + x), 1);
     for (int x = 0; x < 2; ++x) {
@@ -371,6 +370,13 @@ __global__ void __launch_bounds__(kSumThreads, 1)
           load_tile<D>(sb + s * L::stage + L::tile, mc, pc.row(i), bh, b_full + 8 * s, L::half, policy);
           if (++s == L::stages) { s = 0; ph ^= 1; }
         }
+      }
+      // what the scan multiplies by where it passes these pieces
+      for (Walk w(A, bh0, bh1); w.on(); w.next()) {
+        if (A.last[w.job]) continue;
+        const Piece<kT> pc = get_piece<kT>(P, lens, part, w.bh, w.back());
+        reinterpret_cast<float2*>(A.sums[w.job] + i64(P.places()) * D * D)[pc.index] =
+            decay_power2(decay_log2(A.log_decay[w.bh % P.H]), pc.tokens);
       }
     }
   } else if (warp == 17) {
@@ -682,8 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
   const float* const log_decay = A.log_decay;
   const int32_t* const lens = A.lens;
   if (A.zero && tid == 0 && blockIdx.x == 0) *A.zero = 0;
-  const int bh0 = static_cast<int>(P.begin(part) / P.chunks);
-  const int bh1 = static_cast<int>((P.begin(part + 1) - 1) / P.chunks);
+  const int bh0 = P.head(P.begin(part)), bh1 = P.head(P.begin(part + 1) - 1);
   if (tid == 0) {
     for (int x = 0; x < 15; ++x) mbar_init(smem_u32(bars + x), 1);
     mbar_init(b_p, 4);
@@ -702,7 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
   __syncthreads();
   tc_fence_after();
   next_may_launch();
-  wait_for_previous();
   // X under P; Z under O; T, over 16 tokens' columns their hi (8) and lo (8)
   const uint32_t tX = *tslot, tO = tX + 128, tU = tX + 256, tT = tX + 384;
   const Waiter wait{A.status, abort_flag, A.limit};
@@ -842,6 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
     }
   } else if (warp < 12) {
     // ------------------------------------------------ weights and state
+    // The kernel before leaves nothing but the states that these warps read:
+    // the first chunk's loads and X are under way meanwhile.  (The results are
+    // stored behind Z, so behind this as well.)
+    wait_for_previous();
     const int h = (warp - 4) >> 2;       // half of the tokens (T), of the state's columns
     constexpr int CW = D / 2;
     const int col0 = h * CW;
@@ -1082,9 +1090,16 @@ DecayParts decay_parts(const Geom& g, int jobs, bool sums) {
   P.N = g.N;
   P.H = g.H;
   P.chunks = (g.N + kC - 1) / kC;
+  P.BH = g.BH;
   P.total = i64(P.chunks) * g.BH;
   P.parts = static_cast<int>(std::min<i64>(P.total, 148 / jobs));
-  if (sums && i64(P.parts) * jobs <= P.total) P.parts *= jobs;
+  P.finer = 1;
+  if (sums && i64(P.parts) * jobs <= P.total) {
+    P.parts *= jobs;
+    P.finer = jobs;
+  }
+  P.quot = P.total / P.parts;
+  P.rem = static_cast<int>(P.total % P.parts);
   return P;
 }
 

@@ -256,7 +256,7 @@ struct DecayRole {
 };
 struct DecaySums {
   const void *b, *c;
-  float* sums;
+  float* sums;        // [places][d][d], then the pieces' powers of the decay: [places] float2
   float w_sum;
   int e;
   bool reverse;
@@ -279,20 +279,40 @@ bool decay_tc_supported(const Geom& g);
 // The heads' chunks of 128 tokens, in order, are dealt out evenly: CTA k of
 // `parts` takes [begin(k), begin(k + 1)), which heads' ends cut into pieces.
 // Piece (k, bh) has place k + bh in the workspace of sums.
+// (Quotients are estimated in fp32 and put right, or kept: a 64-bit division
+// takes a kernel's start a third of a microsecond.)
+#ifdef __CUDACC__
+#define SLA_HD __host__ __device__
+#else
+#define SLA_HD
+#endif
 struct DecayParts {
-  int N, H;
+  int N, H, BH;
   int chunks, parts;  // chunks per head
+  int finer;          // parts of this that make one of the output kernel's
   i64 total;          // of all heads
-#ifdef __CUDACC__
-  __host__ __device__
-#endif
-  i64 begin(int k) const { return total * k / parts; }
+  i64 quot;           // total = quot * parts + rem
+  int rem;
+  // total * k / parts
+  SLA_HD i64 begin(int k) const { return quot * k + rem * k / parts; }
   // the part that holds chunk g: the last k with begin(k) <= g
-#ifdef __CUDACC__
-  __host__ __device__
-#endif
-  int part(i64 g) const { return static_cast<int>(((g + 1) * parts - 1) / total); }
+  SLA_HD int part(i64 g) const {
+    int k = static_cast<int>(static_cast<float>(g) / static_cast<float>(total) * static_cast<float>(parts));
+    while (k > 0 && begin(k) > g) --k;
+    while (k + 1 < parts && begin(k + 1) <= g) ++k;
+    return k;
+  }
+  // the head that holds it
+  SLA_HD int head(i64 g) const {
+    int bh = static_cast<int>(static_cast<float>(g) / static_cast<float>(chunks));
+    while (i64(bh) * chunks > g) --bh;
+    while (i64(bh + 1) * chunks <= g) ++bh;
+    return bh;
+  }
+  // pieces: places in the workspace of sums
+  SLA_HD int places() const { return parts + BH; }
 };
+#undef SLA_HD
 // Parts of a launch of the output kernel with `jobs` roles, or of the sums
 // that go with it (finer where there are chunks enough, cuts at the same places).
 DecayParts decay_parts(const Geom& g, int jobs, bool sums);
@@ -323,12 +343,10 @@ struct DecayScanJob {
   bool turned;         // `first` is the transpose of the sums
   bool reverse;
 };
-cudaError_t launch_decay_scan(const DecayScanJob& job, const float* log_decay, const int32_t* lens,
-                              const DecayPlan& P, const Geom& g, cudaStream_t s);
+cudaError_t launch_decay_scan(const DecayScanJob& job, const DecayPlan& P, const Geom& g, cudaStream_t s);
 // the same over pieces with packed sums, for one or two jobs; behind
 // launch_decay_sums_tc in the stream
-cudaError_t launch_decay_scan_parts(const DecayScanJob* jobs, int count, const float* log_decay,
-                                    const int32_t* lens, const DecayParts& P, const Geom& g,
+cudaError_t launch_decay_scan_parts(const DecayScanJob* jobs, int count, const DecayParts& P, const Geom& g,
                                     cudaStream_t s);
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                               const int32_t* lens, const float* state_in, float* state_out, void* out,

@@ -191,7 +191,7 @@ DecayWs decay_ws(const Geom& g, bool backward) {
     const sla::DecayPlan P = sla::decay_plan(g);
     states = P.segs > 1 ? size_t(g.BH) * P.segs : 0;
   }
-  states *= sizeof(float) * g.d * g.d;
+  states *= sizeof(float) * g.d * g.d + sizeof(float2);  // each with its power of the decay
   DecayWs w;
   size_t off = kStatusBytes;
   w.sums = off; off = align_up(off + states);
@@ -806,7 +806,7 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
       const sla::DecaySums job{k, v, sums, 1.0f, 0, false};
       const sla::DecayScanJob scan{sums, state_in, state_out, false, false};
       SLA_CUDA(sla::launch_decay_sums_tc(&job, 1, log_decay, lens, P, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan_parts(&scan, 1, log_decay, lens, P, g, s));
+      SLA_CUDA(sla::launch_decay_scan_parts(&scan, 1, P, g, s));
       start = {sums, true};
       zero = nullptr;
     }
@@ -826,7 +826,7 @@ sla_status sla_decay_attention(const sla_params* p, const void* q, const void* k
     return SLA_OK;
   }
   SLA_CUDA(sla::launch_decay_sums_simt({k, v, sums, 1.0f, 0, false}, log_decay, lens, P, g, status, s));
-  SLA_CUDA(sla::launch_decay_scan({sums, state_in, state_out, false, false}, log_decay, lens, P, g, s));
+  SLA_CUDA(sla::launch_decay_scan({sums, state_in, state_out, false, false}, P, g, s));
   SLA_CUDA(sla::launch_decay_out_simt(q, k, v, log_decay, lens, sums, int64_t(P.segs) * g.d * g.d, out,
                                       nullptr, P, R, g, nullptr, s));
   return SLA_OK;
@@ -880,7 +880,7 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
       const sla::DecayScanJob scans[2] = {{rsums, dstate_out, dstate_in, false, true},
                                           {sums, state_in, nullptr, true, false}};
       SLA_CUDA(sla::launch_decay_sums_tc(jobs, 2, log_decay, lens, F, g, status, zero, s));
-      SLA_CUDA(sla::launch_decay_scan_parts(scans, 2, log_decay, lens, F, g, s));
+      SLA_CUDA(sla::launch_decay_scan_parts(scans, 2, F, g, s));
       r_start = {rsums, true};
       s_start = {sums, true};
       Rs.transposed = false;
@@ -903,9 +903,9 @@ sla_status sla_decay_attention_backward(const sla_params* p, const void* q, cons
   if (P.segs > 1) {
     float *sums = at<float>(ws, w.sums), *rsums = at<float>(ws, w.rsums);
     SLA_CUDA(sla::launch_decay_sums_simt({k, v, sums, 1.0f, 0, false}, log_decay, lens, P, g, status, s));
-    SLA_CUDA(sla::launch_decay_scan({sums, state_in, nullptr, false, false}, log_decay, lens, P, g, s));
+    SLA_CUDA(sla::launch_decay_scan({sums, state_in, nullptr, false, false}, P, g, s));
     SLA_CUDA(sla::launch_decay_sums_simt({q, dout, rsums, g.scale, 1, true}, log_decay, lens, P, g, nullptr, s));
-    SLA_CUDA(sla::launch_decay_scan({rsums, dstate_out, dstate_in, false, true}, log_decay, lens, P, g, s));
+    SLA_CUDA(sla::launch_decay_scan({rsums, dstate_out, dstate_in, false, true}, P, g, s));
     s0 = sums;
     r0 = rsums;
     stride = P.segs * one;
