@@ -707,6 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
   __syncthreads();
   tc_fence_after();
   next_may_launch();
+  // (All of the CTA, though only the state comes from the kernel before: with the
+  // first loads ahead of it, 12 heads of 32,760 took 143 us for 140, the scan's
+  // traffic beside theirs, and 3 heads of 500 17.3 for 18.0.)
+  wait_for_previous();
   // X under P; Z under O; T, over 16 tokens' columns their hi (8) and lo (8)
   const uint32_t tX = *tslot, tO = tX + 128, tU = tX + 256, tT = tX + 384;
   const Waiter wait{A.status, abort_flag, A.limit};
@@ -846,10 +850,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_out_tc(const __grid_constan
     }
   } else if (warp < 12) {
     // ------------------------------------------------ weights and state
-    // The kernel before leaves nothing but the states that these warps read:
-    // the first chunk's loads and X are under way meanwhile.  (The results are
-    // stored behind Z, so behind this as well.)
-    wait_for_previous();
     const int h = (warp - 4) >> 2;       // half of the tokens (T), of the state's columns
     constexpr int CW = D / 2;
     const int col0 = h * CW;
