@@ -237,8 +237,8 @@ __device__ __forceinline__ void take_part(float* v, uint32_t* part) {
 // The tensor core truncates as it accumulates: one chain over ten thousand
 // tokens loses 2^-17 of the sum.  So every two steps the accumulator (two of
 // them, in turn) is added to fp32 registers, and within a step the small parts
-// go first: states are off by at most 3.7e-7 (norm, over lengths to 56,000;
-// fp32 products in a row 1.4e-6).  Every four steps 9.3e-7 and 1 % less time,
+// go first: states are off by at most 3.7e-7 (norm, lengths to 56,000; the same
+// sums in plain fp32 by 1.3e-6).  Every four steps 9.3e-7 and 1 % less time,
 // every step 1.7e-7 and 2 % more.
 constexpr int kThreads = 576;      // 16 worker warps, loader, issuer
 constexpr int kSumThreads = 608;   // ... and two issuers

@@ -428,3 +428,38 @@ def test_gradient_state_in_place():
         torch.cuda.synchronize()
         for got, name in ((dq, "dq"), (dk, "dk"), (dv, "dv"), (both, "dstate")):
             assert torch.equal(got, want[name]), (dtype, name)
+
+
+@pytest.mark.parametrize("B,H,N,d", [(1, 1, 20011, 128),   # one head in 148 pieces (147 in the backward)
+                                     (1, 3, 19100, 64),    # ... three in 50 each
+                                     (2, 90, 257, 64)])    # heads that the parts' ends cut now and then
+def test_heads_in_many_pieces_and_their_gradients(B, H, N, d):
+    q, k, v, do = (randn(60 + i, B, H, N, d, dtype=BF) for i in range(4))
+    s0, ds = randn(70, B, H, d, d), randn(71, B, H, d, d)
+    g = torch.log1p(-torch.exp2(-torch.linspace(7, 13, H))).cuda()
+    p = sla.token_params(B, H, N, d, BF)
+    f = sla.decay_attention(p, q, k, v, g, state=s0)
+    b = sla.decay_attention_backward(p, q, k, v, g, do, state=s0, dstate=ds)
+    scale, t = d ** -0.5, torch.arange(N, device="cuda", dtype=torch.float64)
+
+    def close(got, want, rel, what):
+        off = torch.linalg.norm(got.double() - want) / torch.linalg.norm(want)
+        assert off <= rel, f"{what}: {off:.3g}"
+
+    for bi, h in {(0, 0), (0, H - 1), (B - 1, H // 2)}:
+        a, at = g[h].double(), (bi, h)
+        Q, K, V, DO = (x[at].double() for x in (q, k, v, do))
+        S, R = s0[at].double(), ds[at].double()
+        here, left = torch.exp(a * (t + 1))[:, None], torch.exp(a * (N - 1 - t))[:, None]
+        end = torch.exp(a * N)
+        # (three roundings of half a bf16 step at most, states to fp32 accuracy)
+        out, state = _long_reference(Q, K, V, a, scale)
+        close(f["out"][at], out + scale * here * (Q @ S), 3 * 2.0 ** -8, "out")
+        close(f["state"][at], state + end * S, 2.0 ** -19, "state")
+        dq, _ = _long_reference(DO, V, K, a, scale)
+        close(b["dq"][at], dq + scale * here * (DO @ S.T), 3 * 2.0 ** -8, "dq")
+        dv, r = _long_reference(K.flip(0), Q.flip(0), DO.flip(0), a, scale)
+        close(b["dv"][at], dv.flip(0) + left * (K @ R), 3 * 2.0 ** -8, "dv")
+        dk, _ = _long_reference(V.flip(0), DO.flip(0), Q.flip(0), a, scale)
+        close(b["dk"][at], dk.flip(0) + left * (V @ R.T), 3 * 2.0 ** -8, "dk")
+        close(b["dstate"][at], scale * torch.exp(a) * r + end * R, 2.0 ** -19, "gradient of the state")
