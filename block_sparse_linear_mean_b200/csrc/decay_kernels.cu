@@ -541,12 +541,13 @@ cudaError_t launch_decay_out_simt(const void* a, const void* b, const void* c, c
 template <typename Segments>
 cudaError_t launch_scan(const DecayScanJob& j0, const DecayScanJob& j1, int jobs, const Segments& G, int most,
                         const Geom& g, cudaStream_t s) {
+  constexpr size_t each = 128 * sizeof(float4) + sizeof(float2);
   const int room = std::min(most, kScan);
-  const size_t smem = room * (128 * sizeof(float4) + sizeof(float2));
+  // (the same limit in every call: another thread's may come in between)
   cudaError_t e = cudaFuncSetAttribute(decay_scan_kernel<Segments>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       static_cast<int>(kScan * each));
   if (e != cudaSuccess) return e;
-  return launch_behind(true, decay_scan_kernel<Segments>, dim3(g.d * g.d / 512, g.BH, jobs), 128, smem, s, j0, j1,
+  return launch_behind(true, decay_scan_kernel<Segments>, dim3(g.d * g.d / 512, g.BH, jobs), 128, room * each, s, j0, j1,
                        G, g.d, room);
 }
 

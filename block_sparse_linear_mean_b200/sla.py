@@ -633,12 +633,12 @@ _Strides = ctypes.c_int64 * 3
 
 
 def _rotary_call(p, r, raw, rot, positions, perm, inverse):
+    if len(raw) != len(rot) or not 1 <= len(raw) <= 2:
+        raise ValueError("one or two tensors on both sides")
     x, z = raw[0], rot[0]
     dev = _cuda(x, "q")
     shape = (p.B, p.H, p.N, p.d)
     dtype = _TORCH_DTYPES[p.dtype]
-    if len(raw) != len(rot) or not 1 <= len(raw) <= 2:
-        raise ValueError("one or two tensors on both sides")
     _want(x, "raw side", shape, dtype, dev, dense=False)
     _want(z, "turned side", shape, z.dtype, dev)
     strides = x.stride()

@@ -463,3 +463,38 @@ def test_heads_in_many_pieces_and_their_gradients(B, H, N, d):
         dk, _ = _long_reference(V.flip(0), DO.flip(0), Q.flip(0), a, scale)
         close(b["dk"][at], dk.flip(0) + left * (V @ R.T), 3 * 2.0 ** -8, "dk")
         close(b["dstate"][at], scale * torch.exp(a) * r + end * R, 2.0 ** -19, "gradient of the state")
+
+
+def test_two_host_threads():
+    """Calls of different shapes from two threads at once, each on a stream of
+    its own: what one sets for its launches is not the other's."""
+    import threading
+    shapes = [(1, 1, 10000, 128), (2, 40, 200, 128)]  # many pieces of one head, two of many
+    jobs = []
+    for n, (B, H, N, d) in enumerate(shapes):
+        q, k, v = (randn(80 + 3 * n + i, B, H, N, d, dtype=BF) for i in range(3))
+        p, g = sla.token_params(B, H, N, d, BF), decays(H)
+        jobs.append((p, q, k, v, g, sla.decay_attention(p, q, k, v, g)))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(job):
+        p, q, k, v, g, want = job
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()) as _:
+                ws = None
+                for _ in range(100):
+                    f = sla.decay_attention(p, q, k, v, g, ws=ws)
+                    ws = f["ws"]
+                torch.cuda.current_stream().synchronize()
+                if not (torch.equal(f["out"], want["out"]) and torch.equal(f["state"], want["state"])):
+                    failed.append("other results")
+        except Exception as e:  # noqa: BLE001 (reported below)
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
